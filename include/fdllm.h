@@ -22,6 +22,11 @@
  *   fdllm_track_select the tracked set of the next step: the decoded slots the
  *                      masked queries attend to most ([review] "How It Works",
  *                      Step 1: Cache selection).
+ *   fdllm_cache_write_fp8, fdllm_cache_read_fp8, fdllm_tree_attend,
+ *   fdllm_tree_attend_fp8, fdllm_chain_verify, fdllm_tree_verify
+ *                      speculative decoding next to it: an 8-bit cache, a tree of
+ *                      drafted tokens over it, and sampled acceptance.  The pages
+ *                      have no counterpart.
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer owned by the caller, unless
@@ -259,6 +264,141 @@ fdllm_status fdllm_track_select(int B, int N, int H, int dh, int nq, int dtype,
                                 const int8_t* q_masked, const int8_t* candidate,
                                 const void* k_cache, int beta_t, int32_t* track, float* mass,
                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Speculative decoding over a cache: 8-bit rows, a tree of drafted tokens, and
+ * the verification of sampled drafts.  One step of a caller that drafts tokens:
+ * write the drafts' k,v behind the sequence (fdllm_cache_write_fp8 or its own
+ * 16-bit write), attend the tree (fdllm_tree_attend*), form the target's
+ * probabilities, verify (fdllm_chain_verify / fdllm_tree_verify), and write the
+ * accepted nodes' k,v at the slots they end up in.
+ * ------------------------------------------------------------------------- */
+
+/* Workspace of the two calls below (the status header alone; B, R >= 0). */
+size_t fdllm_cache_fp8_workspace_bytes(int B, int R);
+
+/* Quantises rows of k and v as they are written into an 8-bit cache.
+ *   k_rows, v_rows [B, R, H, dh]  fp32 or bf16 (dtype)
+ *   pos      int32 [B, R]         the slot of each row; -1 skips the row (padding)
+ *   k_cache, v_cache [B, H, N, dh] e4m3 (one byte an element)
+ *   k_scale, v_scale float [B, H, N]: an element stands for its value * scale
+ * Each (row, head) of dh values x is kept with a = max |x| (NaN left out),
+ * brought into [2^-96, FLT_MAX]:  scale = a / 448,  element = e4m3(x * (448 / a)),
+ * all in fp32, rounded to the nearest (ties to even), beyond 448 to 448; a NaN
+ * stays a NaN.  Rows of the same slot: the one of the highest index is kept.
+ * A slot outside [0, N) other than -1 sets FDLLM_ERR_BAD_INDEX and its row is
+ * skipped.  dh in {64, 128}.  The other slots keep their values. */
+fdllm_status fdllm_cache_write_fp8(int B, int N, int H, int dh, int R, int dtype,
+                                   const void* k_rows, const void* v_rows, const int32_t* pos,
+                                   void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Reads rows of an 8-bit cache back: k_rows, v_rows [B, R, H, dh] (out, dtype)
+ * = element * scale in fp32, rounded once to dtype.  pos as above, in any order
+ * and repeated at will; rows of pos -1 (or out of range, which sets
+ * FDLLM_ERR_BAD_INDEX) are left as they were. */
+fdllm_status fdllm_cache_read_fp8(int B, int N, int H, int dh, int R, int dtype,
+                                  const int32_t* pos, const void* k_cache, const void* v_cache,
+                                  const float* k_scale, const float* v_scale, void* k_rows,
+                                  void* v_rows, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Largest tree of fdllm_tree_attend* and fdllm_tree_verify. */
+#define FDLLM_MAX_TREE_NODES 256
+/* Largest number of sequences of one fdllm_tree_attend* call. */
+#define FDLLM_MAX_TREE_SEQS 1024
+
+/* Workspace of fdllm_tree_attend and fdllm_tree_attend_fp8 (0 for unsupported
+ * arguments).  One sized for the largest T and B serves smaller ones. */
+size_t fdllm_tree_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int dh, int T, int dtype);
+
+/* Attention of a tree of drafted tokens over a cache with a length per sequence.
+ *   q        [B, T, Hq, dh]       rotated queries of the T nodes
+ *   k_cache, v_cache [B, Hkv, N, dh]; query head h reads kv head h / (Hq / Hkv)
+ *   cache_len int32 [B]           sequence b's tokens lie in slots [0, cache_len[b]);
+ *                                 node t's own k, v in slot cache_len[b] + t
+ *   parent   int32 [B, T]         node t's parent, -1 <= parent < t (-1: the node
+ *                                 hangs below the sequence itself); NULL: every
+ *                                 node's parent is the one before it (a chain)
+ *   n_nodes  int32 [B]            nodes of each sequence, 0..T; NULL: T for all
+ *   out      [B, T, Hq * dh]      out = softmax(q K^T / sqrt(dh)) V over the
+ *                                 sequence's slots, the node's ancestors and itself;
+ *                                 rows of nodes past n_nodes[b] are left as they were
+ * No slot past the sequence's nodes is used, whatever it holds; a sibling's NaN
+ * or infinity reaches no node that does not see it.  T = 1 is single-token
+ * decoding; all nodes of a prompt's chunk may be one chain of T.
+ * Hq a multiple of Hkv, at most 64 query heads to a kv head; T at most
+ * FDLLM_MAX_TREE_NODES; B at most FDLLM_MAX_TREE_SEQS.  A cache_len or n_nodes
+ * out of range (cache_len + n_nodes > N included) sets FDLLM_ERR_BAD_INDEX and
+ * that sequence's rows are left as they were; a parent out of range sets it too
+ * and counts as -1.  Deterministic. */
+fdllm_status fdllm_tree_attend(int B, int N, int Hq, int Hkv, int dh, int T, int dtype,
+                               const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* cache_len, const int32_t* parent,
+                               const int32_t* n_nodes, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* The same over an 8-bit cache as fdllm_cache_write_fp8 leaves it; q and out
+ * bf16 (dtype FDLLM_BF16; fp32 is FDLLM_ERR_UNSUPPORTED). */
+fdllm_status fdllm_tree_attend_fp8(int B, int N, int Hq, int Hkv, int dh, int T, int dtype,
+                                   const void* q, const void* k_cache, const void* v_cache,
+                                   const float* k_scale, const float* v_scale,
+                                   const int32_t* cache_len, const int32_t* parent,
+                                   const int32_t* n_nodes, void* out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Largest chain of fdllm_chain_verify. */
+#define FDLLM_MAX_CHAIN 1024
+
+/* Workspace of fdllm_chain_verify and fdllm_tree_verify (0 for unsupported
+ * arguments). */
+size_t fdllm_draft_verify_workspace_bytes(int B, int T, int V);
+
+/* Verification of sampled drafts: accept each with the odds that keep the
+ * target's distribution, and draw the token after the last accepted one.
+ *   target   float [B, T + 1, V]  the target's probabilities: row i after i drafts
+ *   draft    float [B, T, V]      the distribution that draft i was drawn from
+ *   tok      int32 [B, T]         the drafts
+ *   n_draft  int32 [B]            drafts of each sequence, 0..T; NULL: T for all
+ *   u        float [B, T], r float [B]: given random numbers in [0, 1)
+ *   n_accept int32 [B] out        drafts accepted: i is, while
+ *                                 u[i] * draft[i][tok[i]] < target[i][tok[i]]
+ *   next_tok int32 [B] out        the smallest v whose running sum of w exceeds
+ *                                 r * (the sum of w): w = max(target - draft, 0) of
+ *                                 the row of the first draft not accepted, or the
+ *                                 target's row behind the last draft.  A w that is 0
+ *                                 everywhere: that row of target itself; 0 too: -1.
+ * Products, differences and sums in 64 bits; a NaN counts as 0, and so does a
+ * negative weight.  A token outside [0, V) sets FDLLM_ERR_BAD_INDEX and is not
+ * accepted; an n_draft out of range sets it too and is brought into [0, T].
+ * Deterministic. */
+fdllm_status fdllm_chain_verify(int B, int T, int V, const float* target, const float* draft,
+                                const int32_t* tok, const int32_t* n_draft, const float* u,
+                                const float* r, int32_t* n_accept, int32_t* next_tok,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for a tree of candidates that were not sampled (a node's children are
+ * the likeliest tokens, say): node 0 is the last token that is certain, and row t
+ * of target [B, T, V] is the target's distribution after node t.
+ *   tok, parent int32 [B, T]      node t's token and parent (0 <= parent < t;
+ *                                 those of node 0 are not read)
+ *   n_nodes  int32 [B]            nodes of each sequence, 1..T; NULL: T for all
+ *   u        float [B, T]         node t's number, for the choice among its children
+ *   r        float [B]
+ *   path     int32 [B, T] out     the accepted nodes behind node 0, in order; then -1
+ *   n_accept int32 [B] out        how many
+ *   next_tok int32 [B] out        the token behind the last of them
+ * From node n the walk goes to its first child (by index) c with
+ * u[n] < the sum of target[n][tok] over the children up to c; a sibling that
+ * repeats an earlier one's token adds nothing.  Where none is taken, next_tok is
+ * drawn from target[n] without its children's tokens, as above (their weight 0).
+ * A token or parent out of range sets FDLLM_ERR_BAD_INDEX and the node is never
+ * reached; an n_nodes out of range sets it and is brought into [1, T].  T >= 1. */
+fdllm_status fdllm_tree_verify(int B, int T, int V, const float* target, const int32_t* tok,
+                               const int32_t* parent, const int32_t* n_nodes, const float* u,
+                               const float* r, int32_t* path, int32_t* n_accept,
+                               int32_t* next_tok, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /* Diagnostic: how the bf16 attention of a step with these shapes spreads its
  * work over the current device's SMs (the choice depends only on the shapes and

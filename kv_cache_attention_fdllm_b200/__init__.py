@@ -18,7 +18,10 @@ from .api import (ERR_BAD_INDEX, ERR_CUDA, ERR_INVALID_ARG, ERR_TIMEOUT, ERR_UNS
                   fdllm_fused_step, fdllm_fused_step_rows, fdllm_fused_step_workspace_bytes,
                   fdllm_get_status,
                   fdllm_qkv_rope_scatter, fdllm_verify_attend, fdllm_verify_qkv_rope_scatter,
-                  fdllm_track_select, fdllm_verify_step, fdllm_verify_step_workspace_bytes)
+                  fdllm_track_select, fdllm_verify_step, fdllm_verify_step_workspace_bytes,
+                  fdllm_cache_fp8_workspace_bytes, fdllm_cache_write_fp8, fdllm_cache_read_fp8,
+                  fdllm_tree_attend_workspace_bytes, fdllm_tree_attend, fdllm_tree_attend_fp8,
+                  fdllm_draft_verify_workspace_bytes, fdllm_chain_verify, fdllm_tree_verify)
 
 from .shard import max_over_ranks, rank_sequences  # noqa: E402
 

@@ -38,6 +38,15 @@ SIGNATURES = {
                                                      _vp, _vp, _vp, _vp, _vp]),
     "fdllm_track_select": (_c_int, [_c_int] * 6 + [_vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_size,
                                                     _vp]),
+    "fdllm_cache_fp8_workspace_bytes": (_c_size, [_c_int] * 2),
+    "fdllm_cache_write_fp8": (_c_int, [_c_int] * 6 + [_vp] * 8 + [_c_size, _vp]),
+    "fdllm_cache_read_fp8": (_c_int, [_c_int] * 6 + [_vp] * 8 + [_c_size, _vp]),
+    "fdllm_tree_attend_workspace_bytes": (_c_size, [_c_int] * 7),
+    "fdllm_tree_attend": (_c_int, [_c_int] * 7 + [_vp] * 8 + [_c_size, _vp]),
+    "fdllm_tree_attend_fp8": (_c_int, [_c_int] * 7 + [_vp] * 10 + [_c_size, _vp]),
+    "fdllm_draft_verify_workspace_bytes": (_c_size, [_c_int] * 3),
+    "fdllm_chain_verify": (_c_int, [_c_int] * 3 + [_vp] * 9 + [_c_size, _vp]),
+    "fdllm_tree_verify": (_c_int, [_c_int] * 3 + [_vp] * 10 + [_c_size, _vp]),
     "fdllm_attention_split": (_c_int, [_c_int] * 7 + [_vp]),
     "fdllm_bounded_wait_selftest": (_c_int, [ctypes.c_uint64, _vp, _c_size, _vp]),
     "fdllm_launch_count": (ctypes.c_uint64, []),

@@ -66,6 +66,11 @@ def _need(t, name, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {tuple(t.shape)}")
+
+
 def _dtype_code(t):
     if t.dtype not in _DT:
         raise ValueError(f"unsupported storage dtype {t.dtype}")
@@ -321,6 +326,173 @@ def fdllm_accept_noalloc(logits, kind, ref_tok, rank, top1, conf, flags, n_accep
                                     _p(n_accept), _stream(stream, dev))
     _check(st, "fdllm_accept_noalloc")
     return top1, conf, flags, n_accept
+
+
+# ---------------------------------------------------------------- drafted tokens over a cache
+
+def fdllm_cache_fp8_workspace_bytes(B, R) -> int:
+    return int(lib().fdllm_cache_fp8_workspace_bytes(B, R))
+
+
+def fdllm_tree_attend_workspace_bytes(B, N, Hq, Hkv, dh, T, dtype) -> int:
+    return int(lib().fdllm_tree_attend_workspace_bytes(B, N, Hq, Hkv, dh, T,
+                                                       _DT.get(dtype, dtype)))
+
+
+def fdllm_draft_verify_workspace_bytes(B, T, V) -> int:
+    return int(lib().fdllm_draft_verify_workspace_bytes(B, T, V))
+
+
+def _check_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace):
+    _need(k_rows, "k_rows")
+    _dims(k_rows, "k_rows", 4)
+    B, R, H, dh = k_rows.shape
+    dev = k_rows.device
+    _need(v_rows, "v_rows", k_rows.dtype, (B, R, H, dh), dev)
+    _need(pos, "pos", torch.int32, (B, R), dev)
+    _need(k_cache, "k_cache", torch.float8_e4m3fn)
+    _dims(k_cache, "k_cache", 4)
+    N = k_cache.shape[2]
+    _need(k_cache, "k_cache", torch.float8_e4m3fn, (B, H, N, dh), dev)
+    _need(v_cache, "v_cache", torch.float8_e4m3fn, (B, H, N, dh), dev)
+    _need(k_scale, "k_scale", torch.float32, (B, H, N), dev)
+    _need(v_scale, "v_scale", torch.float32, (B, H, N), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    return B, N, H, dh, R
+
+
+def fdllm_cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace,
+                          stream=None):
+    """Rows of k and v quantised into an 8-bit cache at pos (see include/fdllm.h).
+
+    k_rows, v_rows [B, R, H, dh]; pos int32 [B, R], -1 skips a row; the caches
+    float8_e4m3fn [B, H, N, dh] with float32 scales [B, H, N], updated in place."""
+    B, N, H, dh, R = _check_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
+    st = lib().fdllm_cache_write_fp8(B, N, H, dh, R, _dtype_code(k_rows), _p(k_rows), _p(v_rows),
+                                     _p(pos), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
+                                     _p(workspace), workspace.numel(),
+                                     _stream(stream, k_rows.device))
+    _check(st, "fdllm_cache_write_fp8")
+
+
+def fdllm_cache_read_fp8(pos, k_cache, v_cache, k_scale, v_scale, k_rows, v_rows, workspace,
+                         stream=None):
+    """Rows of an 8-bit cache read back into k_rows, v_rows [B, R, H, dh] (see include/fdllm.h)."""
+    B, N, H, dh, R = _check_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
+    st = lib().fdllm_cache_read_fp8(B, N, H, dh, R, _dtype_code(k_rows), _p(pos), _p(k_cache),
+                                    _p(v_cache), _p(k_scale), _p(v_scale), _p(k_rows), _p(v_rows),
+                                    _p(workspace), workspace.numel(),
+                                    _stream(stream, k_rows.device))
+    _check(st, "fdllm_cache_read_fp8")
+    return k_rows, v_rows
+
+
+def _check_tree(q, k_cache, v_cache, cache_dtype, cache_len, parent, n_nodes, out, workspace):
+    _need(q, "q")
+    _dims(q, "q", 4)
+    B, T, Hq, dh = q.shape
+    dev = q.device
+    _need(k_cache, "k_cache", cache_dtype)
+    _dims(k_cache, "k_cache", 4)
+    Hkv, N = k_cache.shape[1], k_cache.shape[2]
+    _need(k_cache, "k_cache", cache_dtype, (B, Hkv, N, dh), dev)
+    _need(v_cache, "v_cache", cache_dtype, (B, Hkv, N, dh), dev)
+    _need(cache_len, "cache_len", torch.int32, (B,), dev)
+    if parent is not None:
+        _need(parent, "parent", torch.int32, (B, T), dev)
+    if n_nodes is not None:
+        _need(n_nodes, "n_nodes", torch.int32, (B,), dev)
+    _need(out, "out", q.dtype, (B, T, Hq * dh), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    return B, N, Hq, Hkv, dh, T
+
+
+def fdllm_tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, workspace,
+                      stream=None):
+    """Attention of a tree of drafted tokens over a cache (see include/fdllm.h).
+
+    q [B, T, Hq, dh]; caches [B, Hkv, N, dh]; cache_len int32 [B]; parent int32
+    [B, T] or None (a chain); n_nodes int32 [B] or None (T); out [B, T, Hq*dh]."""
+    B, N, Hq, Hkv, dh, T = _check_tree(q, k_cache, v_cache, q.dtype, cache_len, parent, n_nodes,
+                                       out, workspace)
+    st = lib().fdllm_tree_attend(B, N, Hq, Hkv, dh, T, _dtype_code(q), _p(q), _p(k_cache),
+                                 _p(v_cache), _p(cache_len), _p(parent), _p(n_nodes), _p(out),
+                                 _p(workspace), workspace.numel(), _stream(stream, q.device))
+    _check(st, "fdllm_tree_attend")
+    return out
+
+
+def fdllm_tree_attend_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_len, parent, n_nodes, out,
+                          workspace, stream=None):
+    """fdllm_tree_attend over an 8-bit cache (float8_e4m3fn, float32 scales [B, Hkv, N])."""
+    B, N, Hq, Hkv, dh, T = _check_tree(q, k_cache, v_cache, torch.float8_e4m3fn, cache_len, parent,
+                                       n_nodes, out, workspace)
+    _need(k_scale, "k_scale", torch.float32, (B, Hkv, N), q.device)
+    _need(v_scale, "v_scale", torch.float32, (B, Hkv, N), q.device)
+    st = lib().fdllm_tree_attend_fp8(B, N, Hq, Hkv, dh, T, _dtype_code(q), _p(q), _p(k_cache),
+                                     _p(v_cache), _p(k_scale), _p(v_scale), _p(cache_len),
+                                     _p(parent), _p(n_nodes), _p(out), _p(workspace),
+                                     workspace.numel(), _stream(stream, q.device))
+    _check(st, "fdllm_tree_attend_fp8")
+    return out
+
+
+def fdllm_chain_verify(target, draft, tok, n_draft, u, r, n_accept, next_tok, workspace,
+                       stream=None):
+    """Sampled acceptance of a drafted chain (see include/fdllm.h).
+
+    target float32 [B, T+1, V], draft float32 [B, T, V], tok int32 [B, T], n_draft
+    int32 [B] or None (T), u float32 [B, T], r float32 [B]; n_accept, next_tok
+    int32 [B] (out)."""
+    _need(target, "target", torch.float32)
+    _dims(target, "target", 3)
+    _need(draft, "draft", torch.float32)
+    _dims(draft, "draft", 3)
+    B, T, V = draft.shape
+    dev = target.device
+    _need(target, "target", torch.float32, (B, T + 1, V))
+    _need(draft, "draft", torch.float32, (B, T, V), dev)
+    _need(tok, "tok", torch.int32, (B, T), dev)
+    if n_draft is not None:
+        _need(n_draft, "n_draft", torch.int32, (B,), dev)
+    _need(u, "u", torch.float32, (B, T), dev)
+    _need(r, "r", torch.float32, (B,), dev)
+    _need(n_accept, "n_accept", torch.int32, (B,), dev)
+    _need(next_tok, "next_tok", torch.int32, (B,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    st = lib().fdllm_chain_verify(B, T, V, _p(target), _p(draft), _p(tok), _p(n_draft), _p(u),
+                                  _p(r), _p(n_accept), _p(next_tok), _p(workspace),
+                                  workspace.numel(), _stream(stream, dev))
+    _check(st, "fdllm_chain_verify")
+    return n_accept, next_tok
+
+
+def fdllm_tree_verify(target, tok, parent, n_nodes, u, r, path, n_accept, next_tok, workspace,
+                      stream=None):
+    """Sampled acceptance along a drafted tree (see include/fdllm.h).
+
+    target float32 [B, T, V], tok and parent int32 [B, T], n_nodes int32 [B] or
+    None (T), u float32 [B, T], r float32 [B]; path int32 [B, T], n_accept and
+    next_tok int32 [B] (out)."""
+    _need(target, "target", torch.float32)
+    _dims(target, "target", 3)
+    B, T, V = target.shape
+    dev = target.device
+    _need(tok, "tok", torch.int32, (B, T), dev)
+    _need(parent, "parent", torch.int32, (B, T), dev)
+    if n_nodes is not None:
+        _need(n_nodes, "n_nodes", torch.int32, (B,), dev)
+    _need(u, "u", torch.float32, (B, T), dev)
+    _need(r, "r", torch.float32, (B,), dev)
+    _need(path, "path", torch.int32, (B, T), dev)
+    _need(n_accept, "n_accept", torch.int32, (B,), dev)
+    _need(next_tok, "next_tok", torch.int32, (B,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    st = lib().fdllm_tree_verify(B, T, V, _p(target), _p(tok), _p(parent), _p(n_nodes), _p(u),
+                                 _p(r), _p(path), _p(n_accept), _p(next_tok), _p(workspace),
+                                 workspace.numel(), _stream(stream, dev))
+    _check(st, "fdllm_tree_verify")
+    return path, n_accept, next_tok
 
 
 SPLIT_STREAM_K, SPLIT_WHOLE_ITEMS, SPLIT_CLUSTERS = 1, 2, 3

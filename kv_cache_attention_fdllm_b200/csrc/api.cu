@@ -5,8 +5,7 @@
 
 #include <atomic>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "api_util.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -16,15 +15,6 @@ namespace {
 
 constexpr int kVersion = 100;  // 0.1.0
 constexpr int kMaxVerifyRows = 512;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// An NVTX range around each entry point, so that a profiler's timeline shows
-// which call launched which kernels (a no-op when no tool is attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-};
 
 size_t elt_size(int dtype) { return dtype == FDLLM_F32 ? 4 : 2; }
 
@@ -69,16 +59,6 @@ Layout step_layout(int B, int N, int D, int H, int dh, int rows, int S_max, int 
   return L;
 }
 
-fdllm_status check_ws(void* ws, size_t bytes, size_t need) {
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < need)
-    return FDLLM_ERR_WORKSPACE;
-  return FDLLM_OK;
-}
-
-fdllm_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FDLLM_OK : FDLLM_ERR_CUDA; }
-
-char* ws_at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
-
 fdllm_status run_proj(int B, int N, int D, int H, int dh, int rows, int S_max, int verify,
                       int dtype, const void* x, const int32_t* idx, const int8_t* view,
                       const void* w, float rope_base, void* k_cache, void* v_cache,
@@ -112,12 +92,6 @@ fdllm_status run_attn(int B, int N, int H, int dh, int rows, int S_max, int veri
   a.ws = ws_at(ws, L.attn_off);
   a.ws_bytes = L.attn_bytes;
   return from_cuda(launch_attn(a, stream));
-}
-
-bool all_aligned(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (!p || !aligned16(p)) return false;
-  return true;
 }
 
 fdllm_status check_verify_extra(int R, int S_max, int causal) {

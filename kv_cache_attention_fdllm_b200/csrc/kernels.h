@@ -110,6 +110,64 @@ struct TrackArgs {
 size_t track_workspace_bytes(int B, int N, int H);
 cudaError_t launch_track(const TrackArgs& a, cudaStream_t stream);
 
+// ----------------------------------------------------------------- 8-bit cache rows
+struct CacheFp8Args {
+  int B, N, H, dh, R, dtype;
+  const int32_t* pos;       // [B, R], -1 skips a row
+  void* k_rows;             // [B, R, H, dh]; only read by the write
+  void* v_rows;
+  uint8_t* k_cache;         // e4m3 [B, H, N, dh]; only read by the read
+  uint8_t* v_cache;
+  float* k_scale;           // [B, H, N]
+  float* v_scale;
+  int* status;
+};
+cudaError_t launch_cache_write_fp8(const CacheFp8Args& a, cudaStream_t stream);
+cudaError_t launch_cache_read_fp8(const CacheFp8Args& a, cudaStream_t stream);
+
+// ----------------------------------------------------------------- tree attention
+struct TreeAttnArgs {
+  int B, N, Hq, Hkv, dh, T, dtype;
+  int fp8;                  // the cache is e4m3 with scales
+  const void* q;            // [B, T, Hq, dh]
+  const void* k_cache;      // [B, Hkv, N, dh]
+  const void* v_cache;
+  const float* k_scale;     // fp8: [B, Hkv, N]
+  const float* v_scale;
+  const int32_t* cache_len; // [B]
+  const int32_t* parent;    // [B, T] or null (chain)
+  const int32_t* n_nodes;   // [B] or null (T)
+  void* out;                // [B, T, Hq*dh]
+  int* status;
+  void* ws;
+  size_t ws_bytes;
+};
+cudaError_t launch_tree_simt(const TreeAttnArgs& a, cudaStream_t stream);
+
+// ----------------------------------------------------------------- sampled verification
+struct DraftVerifyArgs {
+  int B, T, V;
+  const float* target;      // chain [B, T+1, V], tree [B, T, V]
+  const float* draft;       // chain [B, T, V]; tree: null
+  const int32_t* tok;       // [B, T]
+  const int32_t* parent;    // tree [B, T]
+  const int32_t* count;     // [B] or null: drafts (chain) or nodes (tree) of a sequence
+  const float* u;           // [B, T]
+  const float* r;           // [B]
+  int32_t* path;            // tree [B, T]
+  int32_t* n_accept;        // [B]
+  int32_t* next_tok;        // [B]
+  int* status;
+  unsigned* seq_cnt;        // [kMaxVerifySeqs], zero between calls
+  double* parts;            // [B][sub-blocks of a row]
+};
+// Sequences of one call.  The counters have their place whatever the shapes are,
+// so that calls of different shapes share a workspace.
+constexpr int kMaxVerifySeqs = 16384;
+size_t draft_verify_parts_bytes(int B, int V);
+cudaError_t launch_chain_verify(const DraftVerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_verify(const DraftVerifyArgs& a, cudaStream_t stream);
+
 // ----------------------------------------------------------------- kernel families
 size_t proj_simt_workspace_bytes(int M, int H, int dh);
 size_t proj_tc_workspace_bytes(int M, int D, int H, int dh, int num_sms);
