@@ -28,6 +28,10 @@ fdllm_status check_tree(int B, int N, int Hq, int Hkv, int dh, int T, int dtype)
   if (T > FDLLM_MAX_TREE_NODES || B > FDLLM_MAX_TREE_SEQS || Hq / Hkv > 64 || Hq > 4096)
     return FDLLM_ERR_UNSUPPORTED;
   if ((long long)B * N > (1ll << 31) || N > (1 << 30)) return FDLLM_ERR_UNSUPPORTED;
+  // work units (chunk of at most 64 rows of whole nodes, sequence, kv head, 128 slots)
+  // are counted in 32 bits
+  const int g = Hq / Hkv, tn = 64 / g, chunks = (T + tn - 1) / tn;
+  if ((long long)B * Hkv * ((N + 127) / 128) * chunks > (1ll << 30)) return FDLLM_ERR_UNSUPPORTED;
   return FDLLM_OK;
 }
 
@@ -64,7 +68,8 @@ fdllm_status run_tree(const TreeAttnArgs& args, void* workspace, size_t workspac
   a.status = reinterpret_cast<int*>(workspace);
   a.ws = ws_at(workspace, kWsHeaderBytes);
   a.ws_bytes = need - kWsHeaderBytes;
-  return from_cuda(launch_tree_simt(a, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(a.dtype == FDLLM_F32 ? launch_tree_simt(a, s) : launch_tree_tc(a, s));
 }
 
 }  // namespace
@@ -121,7 +126,8 @@ fdllm_status fdllm_cache_read_fp8(int B, int N, int H, int dh, int R, int dtype,
 
 size_t fdllm_tree_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int dh, int T, int dtype) {
   if (check_tree(B, N, Hq, Hkv, dh, T, dtype) != FDLLM_OK) return 0;
-  return kWsHeaderBytes;
+  if (dtype == FDLLM_F32) return kWsHeaderBytes;
+  return kWsHeaderBytes + tree_tc_workspace_bytes(Hq, Hkv, dh, T, device_sm_count());
 }
 
 fdllm_status fdllm_tree_attend(int B, int N, int Hq, int Hkv, int dh, int T, int dtype,

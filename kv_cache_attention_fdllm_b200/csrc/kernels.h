@@ -142,7 +142,9 @@ struct TreeAttnArgs {
   void* ws;
   size_t ws_bytes;
 };
-cudaError_t launch_tree_simt(const TreeAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_simt(const TreeAttnArgs& a, cudaStream_t stream);  // fp32
+cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream);    // 16 and 8 bits
+size_t tree_tc_workspace_bytes(int Hq, int Hkv, int dh, int T, int num_sms);
 
 // ----------------------------------------------------------------- sampled verification
 struct DraftVerifyArgs {

@@ -29,9 +29,9 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-bool encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims,
-                     const uint64_t* strides_bytes, const uint32_t* box,
-                     CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
+static bool encode_map(CUtensorMapDataType type, CUtensorMap* map, int rank, const void* base,
+                       const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                       CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t gdim[5];
@@ -43,11 +43,25 @@ bool encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_
     estride[i] = 1;
   }
   for (int i = 0; i < rank - 1; ++i) gstride[i] = strides_bytes[i];
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+  const CUresult r = fn(map, type, (cuuint32_t)rank,
                         const_cast<void*>(base), gdim, gstride, bdim, estride,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promo,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims,
+                     const uint64_t* strides_bytes, const uint32_t* box,
+                     CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
+  return encode_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, map, rank, base, dims, strides_bytes, box,
+                    swizzle, promo);
+}
+
+bool encode_u8_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                   CUtensorMapL2promotion promo) {
+  return encode_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, map, rank, base, dims, strides_bytes, box,
+                    swizzle, promo);
 }
 
 }  // namespace fdllm

@@ -12,5 +12,9 @@ namespace fdllm {
 bool encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims,
                      const uint64_t* strides_bytes, const uint32_t* box,
                      CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo);
+// The same for one-byte elements.
+bool encode_u8_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                   CUtensorMapL2promotion promo);
 
 }  // namespace fdllm

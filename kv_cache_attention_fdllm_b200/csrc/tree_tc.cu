@@ -1,0 +1,1398 @@
+// Attention of a tree of drafted tokens over a cache on the 5th-generation tensor
+// cores: a 16-bit cache, or an 8-bit one read as it lies.
+//
+// Mathematics.  A row is a (node, query head) pair; the g = Hq / Hkv heads of a kv
+// head and all nodes share its keys, so an item is (chunk of rows, sequence, kv
+// head) and its units are tiles of 128 slots.  With one thread to a slot,
+//   S^T [128 slots x NQ rows] = K_tile Q^T,   O^T [dh x NQ] += V_tile^T P^T
+// waste nothing on padding when rows are few: the slots are the M of both.  The
+// softmax keeps a running maximum per row that is raised only when a tile exceeds
+// it by 2^kThresh; l sums the weights in fp32 before they are rounded.  The tree's
+// mask is one bit test per score, on the tiles that reach past the sequence.
+//
+// 8 bits (e4m3 elements, a scale per slot): the elements go to the tensor cores as
+// they are, with no conversion pass, because everything else fits around them:
+//   - a slot's scale multiplies one row of S^T, i.e. one thread's scores, and for V
+//     the weights of that thread;
+//   - a bf16 query has 8 significant bits, an e4m3 value 4: q 2^-x = q1 + q2 with both
+//     e4m3 (x per row, so that the row's largest is in [128, 256)) is exact down to
+//     2^-10 against the largest, and S = K q1 + K q2 accumulates in the same place;
+//   - a weight is taken as three e5m2 parts (3 significant bits each, of its fp16
+//     value): 9 bits, as bf16 has 8, over a range of 2^31, so that a long flat rest
+//     far below a sink keeps its weight.  e4m3 parts would lose it (2^17).  The
+//     weights carry the slot's scale relative to a power of two that follows the
+//     scales as the running maximum follows the scores.
+// The second and third parts cost tensor time, of which there is plenty: a tile
+// takes 20 instructions of 32 cycles (its A operand through shared memory) against
+// some 1400 cycles for its bytes from HBM.
+//
+// Work split: persistent stream-K.  Units are laid out chunk by chunk, sequence by
+// sequence, head by head, tile by tile, from the lengths on the device; CTAs take
+// equal contiguous ranges, so any mix of lengths is balanced.  Chunks are outermost:
+// CTAs on different chunks of the same slots run at the same time and share them in
+// L2.  An item split between CTAs leaves (O, m, l) partials in the workspace; the
+// last of its contributors (a counter, nobody waits) merges them in CTA order, so
+// results do not depend on timing.
+//
+//   warp 0      TMA producer: K and V tiles, and the rows' Q (16-bit cache)
+//   warp 1      TMEM; lane 0 issues both products
+//   warps 2..   softmax (NQ / kCols groups of 4 warps), epilogue, merges
+//   then        finisher: counts the partials in
+//   last        (8-bit) splits the next item's Q into its two e4m3 parts
+//
+// O^T is double-buffered in TMEM: an item's result is written two tiles into the
+// next item, off the softmax path.
+//
+// NaN and infinity.  Slots past the sequence's nodes are masked in S and zeroed in V
+// (0 x NaN would be NaN).  A node's V that is not finite is zeroed the same way, since
+// the tensor cores would spread it to rows that do not see it, and added to the
+// outputs of those that do when they are written.
+#include <limits.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+#include "tmap.h"
+
+namespace fdllm {
+
+namespace {
+
+constexpr int kKT = 128;  // slots of a tile
+constexpr int kMaxNodes = FDLLM_MAX_TREE_NODES;
+constexpr int kAncWords = kMaxNodes / 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -3.0e38f;  // maximum of a row that has seen no slot yet (finite: a
+                                   // masked score, -inf, then weighs 2^-inf = 0, not NaN)
+constexpr int kMaxGrid = 1024;     // counters: one a CTA
+constexpr size_t kSmemBudget = 227 * 1024;
+
+struct TreeParams {
+  int B, N, Hq, Hkv, g, T;
+  int n_qc, tn;         // chunks of rows, nodes of a chunk (tn * g rows)
+  int nk, nv;           // stages of the K and V rings
+  int keep;             // tiles are read by several chunks
+  float qk_scale;       // log2(e) / sqrt(dh)
+  const void* q;        // 8-bit cache: read by the splitter
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* cache_len;
+  const int32_t* parent;
+  const int32_t* n_nodes;
+  __nv_bfloat16* out;
+  int* status;
+  unsigned* cnt;        // [kMaxGrid], zero between calls
+  float* partials;      // [grid][2][part_floats]
+};
+
+template <int NQ, int DH, bool FP8>
+struct Cfg {
+  static constexpr int kCols = NQ == 64 ? 32 : (NQ == 48 ? 24 : 16);  // rows of a softmax thread
+  static constexpr int kSmx = 128 * NQ / kCols;
+  static constexpr int kFinisher = 2 + kSmx / 32;  // warp index
+  static constexpr int kAll = 64 + kSmx + 32 + (FP8 ? 32 : 0);
+  static constexpr int kNQP = NQ == 48 ? 64 : NQ;  // columns of a TMEM buffer, of P's layout
+  static constexpr int kBoxes = FP8 ? 1 : DH / 64;
+  static constexpr uint32_t kBoxRow = FP8 ? DH : 128;  // bytes of a slot in a box
+  static constexpr uint32_t kBoxBytes = kKT * kBoxRow;
+  static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kQBufs = FP8 ? 2 : 1;
+  static constexpr int kQParts = FP8 ? 2 : 1;
+  static constexpr uint32_t kQPart = NQ * (FP8 ? DH : DH * 2);
+  static constexpr uint32_t kQBytes = (kQBufs * kQParts * kQPart + 1023) / 1024 * 1024;
+  static constexpr int kPParts = FP8 ? 3 : 1;
+  static constexpr uint32_t kPRow = kNQP * (FP8 ? 1 : 2);  // bytes of a slot in P
+  static constexpr uint32_t kPPart = kKT * kPRow;          // a multiple of 1024
+  static constexpr uint32_t kPBuf = kPParts * kPPart;
+  // largest exponent step a weight may exceed the running maximum's by, and the
+  // power of two weights are kept at (8 bits: below 2^(2+12+1) in fp16 and e5m2)
+  static constexpr float kThresh = FP8 ? 2.f : 8.f;
+  static constexpr int kPOff = FP8 ? 12 : 0;
+  static constexpr int kPartFloats = NQ * DH + 2 * NQ + 4;  // O, m, l, flag (and padding)
+};
+
+// Shared memory behind the tiles (byte offsets of the misc block).
+struct Misc {
+  static constexpr int kBars = 0;        // 46 mbarriers
+  static constexpr int kInts = 384;      // see Ints
+  static constexpr int kM = 512;         // m_run[64], alpha[64], alpha_o[64]
+  static constexpr int kRed = 1280;      // wred[4][64]
+  static constexpr int kSegM = 2304;     // seg_m[2][64], seg_l[2][64]
+  static constexpr int kNode = 3328;     // col_node[64], col_head[64] (bytes)
+  static constexpr int kQsc = 3456;      // qsc[2][64]
+  static constexpr int kAnc = 3968;      // anc[64][kAncWords]
+  static constexpr int kWts = kAnc + 64 * kAncWords * 4;  // [8][64] merge weights
+  static constexpr int kSeq = kWts + 8 * 64 * 4;          // pre[B + 1], len[B], nn[B]
+};
+
+struct Ints {
+  uint32_t tmem;
+  int abort;
+  int merge_u[2];    // first unit of the item in partial slot s that this CTA merges, or -1
+  int seg_u[2];      // a finished segment (by O buffer): its item's first unit,
+  int seg_lo[2];     // its first tile,
+  int seg_hi[2];     // its last,
+  int seg_bad[2];    // whether it met a node's V that is not finite,
+  int seg_e[2];      // and the power of two its weights were taken against
+  int vexp[8];       // exponents of the softmax warps' V scales
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// OR of a predicate over `n` threads at named barrier `id`.
+__device__ __forceinline__ bool bar_any(int id, int n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+// 2^x on the special-function unit (flush-to-zero; 2^-inf = 0, NaN stays)
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, float* v, int w) {
+  if (w >= 16)
+    tc::tmem_ld16(taddr, v);
+  else
+    tc::tmem_ld8(taddr, v);
+}
+__device__ __forceinline__ void tmem_st_chunk(uint32_t taddr, const float* v, int w) {
+  if (w >= 16)
+    tc::tmem_st16(taddr, v);
+  else
+    tc::tmem_st8(taddr, v);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+// two floats as f16 (a in the low half); beyond the largest to infinity
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+// e4m3 of two floats (lo in the low byte) and the floats they stand for
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+  float2 f;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+// byte offset `off` of a tile whose rows have `row` bytes (32, 64 or 128), swizzled
+__device__ __forceinline__ uint32_t swz(uint32_t off, uint32_t row) {
+  return off ^ (((off >> 7) & (row / 16 - 1)) << 4);
+}
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.4028234663852886e38f); }
+
+// Polling loops give up after kWaitLimitNs without progress.
+struct IdleClock {
+  uint64_t t0 = 0;
+  uint32_t spins = 0;
+  __device__ __forceinline__ void reset() { t0 = 0; spins = 0; }
+  __device__ __forceinline__ bool idle(volatile int* abort, int* status) {
+    if ((++spins & 63u) != 0) return true;
+    if (*abort) return false;
+    const uint64_t now = global_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > kWaitLimitNs) {
+      *abort = 1;
+      set_status(status, FDLLM_ERR_TIMEOUT);
+      return false;
+    }
+    return true;
+  }
+};
+
+// First unit of CTA c's range, and the CTA whose range holds unit u (the largest c
+// with lo(c) <= u; a double-precision estimate is put right with exact products).
+__device__ __forceinline__ int unit_lo(int total, int G, int c) {
+  return (int)((long long)total * c / G);
+}
+__device__ __forceinline__ int owner_of(int u, int total, int G) {
+  const long long lim = ((long long)u + 1) * G;
+  int c = (int)((double)(lim - 1) / (double)total);
+  c = c < 0 ? 0 : (c >= G ? G - 1 : c);
+  while (c + 1 < G && (long long)total * (c + 1) < lim) ++c;
+  while (c > 0 && (long long)total * c >= lim) --c;
+  return c;
+}
+
+// Where a unit lies: chunk, sequence, kv head, tile; the sequence's tile count.
+struct Seqs {
+  const int* pre;  // [B + 1] tiles of the sequences in front
+  int B, Hkv, total;  // total: tiles of all sequences (pre[B])
+};
+struct Cursor {
+  int qc, b, h, t, tb;
+  __device__ __forceinline__ void init(int u, const Seqs& s) {
+    const int per = s.total * s.Hkv;
+    qc = u / per;
+    const int rem = u - qc * per;
+    const int tile = rem / s.Hkv;  // b: the last with pre[b] <= tile (its tiles are not 0)
+    int lo = 0, hi = s.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.pre[mid] <= tile) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    tb = s.pre[b + 1] - s.pre[b];
+    const int r = rem - s.pre[b] * s.Hkv;
+    h = r / tb;
+    t = r - h * tb;
+  }
+  __device__ __forceinline__ void next_item(const Seqs& s) {
+    t = 0;
+    if (++h == s.Hkv) {
+      h = 0;
+      do {
+        if (++b == s.B) {
+          b = 0;
+          ++qc;
+        }
+      } while (s.pre[b + 1] == s.pre[b]);
+      tb = s.pre[b + 1] - s.pre[b];
+    }
+  }
+  __device__ __forceinline__ void next(const Seqs& s) {
+    if (++t == tb) next_item(s);
+  }
+};
+
+template <int NQ, int DH, bool FP8>
+__global__ void __launch_bounds__(Cfg<NQ, DH, FP8>::kAll, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_v, TreeParams p) {
+  using C = Cfg<NQ, DH, FP8>;
+  constexpr int kSmx = C::kSmx;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int NK = p.nk, NV = p.nv;
+  uint8_t* k_ring = smem;
+  uint8_t* v_ring = smem + NK * C::kTileBytes;
+  uint8_t* q_buf = v_ring + NV * C::kTileBytes;
+  uint8_t* p_buf = q_buf + C::kQBytes;
+  uint8_t* misc = p_buf + 2 * C::kPBuf;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(misc + Misc::kBars);
+  uint64_t* k_empty = k_full + 8;
+  uint64_t* v_full = k_empty + 8;
+  uint64_t* v_empty = v_full + 8;
+  uint64_t* q_full = v_empty + 8;    // [2]
+  uint64_t* q_empty = q_full + 2;    // [2]
+  uint64_t* s_full = q_empty + 2;    // [2]
+  uint64_t* s_empty = s_full + 2;    // [2]
+  uint64_t* p_full = s_empty + 2;    // [2]
+  uint64_t* pv_done = p_full + 2;    // [2]
+  uint64_t* fin_full = pv_done + 2;  // [2] a partial's stores are issued
+  Ints* I = reinterpret_cast<Ints*>(misc + Misc::kInts);
+  int* abort_flag = &I->abort;
+  float* m_run = reinterpret_cast<float*>(misc + Misc::kM);
+  float* alpha = m_run + 64;    // rescale of l
+  float* alpha_o = alpha + 64;  // rescale of O
+  float* wred = reinterpret_cast<float*>(misc + Misc::kRed);  // [4][64]
+  float* seg_m = reinterpret_cast<float*>(misc + Misc::kSegM);
+  float* seg_l = seg_m + 2 * 64;
+  uint8_t* col_node = misc + Misc::kNode;
+  uint8_t* col_head = col_node + 64;
+  float* qsc = reinterpret_cast<float*>(misc + Misc::kQsc);  // [2][64]
+  uint32_t* anc = reinterpret_cast<uint32_t*>(misc + Misc::kAnc);
+  float* wts = reinterpret_cast<float*>(misc + Misc::kWts);
+  int* s_pre = reinterpret_cast<int*>(misc + Misc::kSeq);
+  int* s_len = s_pre + p.B + 1;
+  int* s_nn = s_len + p.B;
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x;
+  constexpr uint32_t ncols = 4 * C::kNQP < 32 ? 32 : 4 * C::kNQP;  // 64, 128 or 256
+
+  if (tid == 0) {
+    for (int s = 0; s < 8; ++s) {
+      tc::mbar_init(&k_full[s], 1);
+      tc::mbar_init(&k_empty[s], 1);
+      tc::mbar_init(&v_full[s], 1);
+      tc::mbar_init(&v_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&q_full[b], 1);
+      tc::mbar_init(&q_empty[b], 1 + (FP8 ? kSmx / 32 : 0));  // 8 bits: the scales' readers too
+      tc::mbar_init(&s_full[b], 1);
+      tc::mbar_init(&s_empty[b], kSmx / 32);
+      tc::mbar_init(&p_full[b], kSmx / 32);
+      tc::mbar_init(&pv_done[b], 1);
+      tc::mbar_init(&fin_full[b], kSmx / 32);
+    }
+    I->abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) tc::tmem_alloc(&I->tmem, ncols);
+  if (tid < 64) {
+    col_node[tid] = (uint8_t)(tid / p.g);
+    col_head[tid] = (uint8_t)(tid % p.g);
+  }
+  // rows of Q past the chunk's: zeros, whatever the product makes of them is not read
+  for (int i = tid; i < (int)(C::kQBytes / 16); i += C::kAll)
+    reinterpret_cast<uint4*>(q_buf)[i] = make_uint4(0u, 0u, 0u, 0u);
+  tc::fence_proxy_async_smem();
+  if (tid == 64) {
+    tc::prefetch_tmap(&tm_k);
+    tc::prefetch_tmap(&tm_v);
+    if (!FP8) tc::prefetch_tmap(&tm_q);
+  }
+  // nothing that an earlier kernel wrote is read before this
+  tc::griddep_wait();
+  for (int b = tid; b < p.B; b += C::kAll) {
+    int len = p.cache_len[b];
+    int nn = p.n_nodes ? p.n_nodes[b] : p.T;
+    if (len < 0 || nn < 0 || nn > p.T || len > p.N - nn) {
+      if (cta == 0) set_status(p.status, FDLLM_ERR_BAD_INDEX);
+      len = 0;
+      nn = 0;
+    }
+    s_len[b] = len;
+    s_nn[b] = nn;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int x = b < p.B && s_nn[b] > 0 ? (s_len[b] + s_nn[b] + kKT - 1) / kKT : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < p.B) s_pre[b + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s_pre[0] = 0;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = I->tmem;
+  const uint32_t tmem_o = tmem + 2 * C::kNQP;
+  Seqs S;
+  S.pre = s_pre;
+  S.B = p.B;
+  S.Hkv = p.Hkv;
+  S.total = s_pre[p.B];
+  const int U = S.total * p.Hkv * p.n_qc;  // fits: checked on the host for the largest
+  const int G = min((int)gridDim.x, U);
+  const int u0 = cta < G ? unit_lo(U, G, cta) : 0;
+  const int u1 = cta < G ? unit_lo(U, G, cta + 1) : 0;
+  const int T = u1 - u0;
+
+  if (T == 0) {
+    // no work for this CTA (it meets the others at the end)
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol_kv = p.keep ? tc::policy_evict_normal() : tc::policy_evict_first();
+      const uint64_t pol_q = tc::policy_evict_last();
+      int ik = 0, iv = 0, qn = 0;
+      Cursor ck, cv, cq;
+      ck.init(u0, S);
+      cv = ck;
+      cq = ck;
+      int q_left = FP8 ? 0 : T;  // units not yet covered by a loaded Q
+      IdleClock clk;
+      while (iv < T || q_left > 0) {
+        bool progressed = false;
+        if constexpr (!FP8) {
+          if (q_left > 0 && tc::mbar_test(&q_empty[0], ((uint32_t)qn & 1u) ^ 1u)) {
+            const uint32_t bytes = (uint32_t)(p.tn * p.g) * 128u;
+            tc::mbar_arrive_expect_tx(&q_full[0], bytes * C::kBoxes);
+#pragma unroll
+            for (int x = 0; x < C::kBoxes; ++x)
+              tc::tma_load_5d(q_buf + x * NQ * 128, &tm_q, &q_full[0], x * 64, 0, cq.h,
+                              cq.qc * p.tn, cq.b, pol_q);
+            q_left -= cq.tb - cq.t;
+            if (q_left > 0) cq.next_item(S);
+            ++qn;
+            progressed = true;
+          }
+        }
+        if (ik < T) {
+          const int ks = ik % NK;
+          if (tc::mbar_test(&k_empty[ks], ((uint32_t)(ik / NK) & 1u) ^ 1u)) {
+            uint8_t* kd = k_ring + ks * C::kTileBytes;
+            tc::mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
+#pragma unroll
+            for (int x = 0; x < C::kBoxes; ++x)
+              tc::tma_load_3d(kd + x * C::kBoxBytes, &tm_k, &k_full[ks], x * 64, ck.t * kKT,
+                              ck.b * p.Hkv + ck.h, pol_kv);
+            if (++ik < T) ck.next(S);
+            progressed = true;
+          }
+        }
+        if (iv < ik) {
+          const int vs = iv % NV;
+          if (tc::mbar_test(&v_empty[vs], ((uint32_t)(iv / NV) & 1u) ^ 1u)) {
+            uint8_t* vd = v_ring + vs * C::kTileBytes;
+            tc::mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
+#pragma unroll
+            for (int x = 0; x < C::kBoxes; ++x)
+              tc::tma_load_3d(vd + x * C::kBoxBytes, &tm_v, &v_full[vs], x * 64, cv.t * kKT,
+                              cv.b * p.Hkv + cv.h, pol_kv);
+            if (++iv < T) cv.next(S);
+            progressed = true;
+          }
+        }
+        if (!progressed && !clk.idle(abort_flag, p.status)) break;
+        if (progressed) clk.reset();
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    // Two in-order streams, QK(i) and PV(j), each issued as soon as its inputs are
+    // ready.
+    if (lane == 0) {
+      constexpr uint32_t swz_code = C::kBoxRow == 128 ? 2u : 4u;
+      constexpr uint32_t p_swz = C::kPRow == 128 ? 2u : (C::kPRow == 64 ? 4u : 6u);
+      const uint32_t p_addr = tc::smem_u32(p_buf);
+      int iq = 0, ip = 0, seg = -1, pseg = -1;
+      Cursor cq, cpv;
+      cq.init(u0, S);
+      cpv = cq;
+      IdleClock clk;
+      while (ip < T) {
+        bool progressed = false;
+        if (iq < T) {
+          const bool first = (iq == 0 || cq.t == 0);
+          const bool last = (iq == T - 1 || cq.t == cq.tb - 1);
+          const int qseg = first ? seg + 1 : seg;
+          const int qb = qseg % C::kQBufs;
+          const int ks = iq % NK, sb = iq & 1;
+          if (tc::mbar_test(&k_full[ks], (uint32_t)(iq / NK) & 1u) &&
+              tc::mbar_test(&s_empty[sb], ((uint32_t)(iq >> 1) & 1u) ^ 1u) &&
+              (!first || tc::mbar_test(&q_full[qb], (uint32_t)(qseg / C::kQBufs) & 1u))) {
+            seg = qseg;
+            tc::tc_fence_after();
+            const uint32_t k_addr = tc::smem_u32(k_ring + ks * C::kTileBytes);
+            const uint32_t q_addr = tc::smem_u32(q_buf) + qb * C::kQParts * C::kQPart;
+            const uint32_t d = tmem + sb * C::kNQP;
+            if constexpr (FP8) {
+              constexpr uint32_t idesc = tc::idesc_f8(kKT, NQ, false);
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < DH / 32; ++kk)
+                  tc::mma_f8(d, tc::smem_desc(k_addr + kk * 32, 16, 8 * DH, swz_code),
+                             tc::smem_desc(q_addr + part * C::kQPart + kk * 32, 16, 8 * DH, swz_code),
+                             idesc, part + kk != 0);
+            } else {
+              constexpr uint32_t idesc = tc::idesc_bf16(kKT, NQ, false, false);
+#pragma unroll
+              for (int kk = 0; kk < DH / 16; ++kk) {
+                const uint32_t ko = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
+                const uint32_t qo = (kk >> 2) * NQ * 128 + (kk & 3) * 32;
+                tc::mma_bf16(d, tc::smem_desc(k_addr + ko, 16, 1024, 2),
+                             tc::smem_desc(q_addr + qo, 16, 1024, 2), idesc, kk != 0);
+              }
+            }
+            tc::mma_commit(&s_full[sb]);
+            tc::mma_commit(&k_empty[ks]);
+            if (last) tc::mma_commit(&q_empty[qb]);
+            if (++iq < T) cq.next(S);
+            progressed = true;
+          }
+        }
+        if (ip < iq) {
+          const int vs = ip % NV;
+          if (tc::mbar_test(&p_full[ip & 1], (uint32_t)(ip >> 1) & 1u) &&
+              tc::mbar_test(&v_full[vs], (uint32_t)(ip / NV) & 1u)) {
+            const bool first = (ip == 0 || cpv.t == 0);
+            if (first) ++pseg;
+            tc::tc_fence_after();
+            const uint32_t v_addr = tc::smem_u32(v_ring + vs * C::kTileBytes);
+            const uint32_t pb_addr = p_addr + (ip & 1) * C::kPBuf;
+            const uint32_t o_addr = tmem_o + (uint32_t)((pseg & 1) * C::kNQP);
+            if constexpr (FP8) {
+              constexpr uint32_t idesc = tc::idesc_f8(kKT, NQ, true, true, true);
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int kk = 0; kk < kKT / 32; ++kk)
+                  tc::mma_f8(o_addr, tc::smem_desc(v_addr + kk * 32 * DH, 0, 8 * DH, swz_code),
+                             tc::smem_desc(pb_addr + part * C::kPPart + kk * 32 * C::kPRow, 0,
+                                           8 * C::kPRow, p_swz),
+                             idesc, (first && part + kk == 0) ? 0u : 1u);
+            } else {
+              constexpr uint32_t idesc = tc::idesc_bf16(kKT, NQ, true, true);
+#pragma unroll
+              for (int kk = 0; kk < kKT / 16; ++kk) {
+                const uint64_t da = tc::smem_desc(v_addr + kk * 2048, DH == 128 ? 16384 : 0, 1024, 2);
+                const uint64_t db = tc::smem_desc(pb_addr + kk * 16 * C::kPRow, 0, 8 * C::kPRow, p_swz);
+                tc::mma_bf16(o_addr, da, db, idesc, (first && kk == 0) ? 0u : 1u);
+              }
+            }
+            tc::mma_commit(&pv_done[ip & 1]);
+            tc::mma_commit(&v_empty[vs]);
+            if (++ip < T) cpv.next(S);
+            progressed = true;
+          }
+        }
+        if (!progressed && !clk.idle(abort_flag, p.status)) break;
+        if (progressed) clk.reset();
+      }
+    }
+  } else if (warp < C::kFinisher) {
+    // ------------------------------------------------------------ softmax / epilogue
+    // The warps that share a TMEM lane quarter split the rows: a thread owns one
+    // slot (later one dh row) and the NQH columns [c0, c0 + NQH).
+    constexpr int NQH = C::kCols;
+    const int st = tid - 64;                 // 0..kSmx-1
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;        // column group
+    const int c0 = half * NQH;
+    const int kl = quarter * 32 + lane;      // TMEM lane: slot of S^T, dh row of O^T
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    float l[NQH], mrun[NQH];
+#pragma unroll
+    for (int c = 0; c < NQH; ++c) {
+      l[c] = 0.f;
+      mrun[c] = kNone;
+    }
+    int e_ref = -1000;     // power of two that the segment's weights are taken against
+    int seg = -1;
+    int anc_key = -1;      // (chunk, sequence) whose ancestors are in shared memory
+    int pv_waited = -1;    // index of the last PV this thread waited for
+    int seg_t0 = 0;        // tile at which the segment started
+    int n_done = 0;        // segments whose last tile is through
+    int n_fin = 0;         // segments whose result is written
+    int end0 = 0, end1 = 0;  // last tile (range index) of the segment in O buffer 0 / 1
+    Cursor cs;
+    cs.init(u0, S);
+    const int item0 = u0 - cs.t;  // first unit of the item the range starts in
+
+    // Sum of the values of column c's visible nodes that are not finite, at dh row kl
+    // (0 without any): re-read from the cache, for the rare item that has some.
+    auto unfit = [&](const Cursor& at, int c) -> float {
+      float sum = 0.f;
+      const int len = s_len[at.b], nn = s_nn[at.b];
+      int n = at.qc * p.tn + (int)col_node[c];
+      if (n >= nn) return 0.f;
+      const size_t head = ((size_t)at.b * p.Hkv + at.h) * p.N + len;
+      while (n >= 0) {
+        float v;
+        if constexpr (FP8)
+          v = from_e4m3x2(static_cast<const uint8_t*>(p.v_cache)[(head + n) * DH + kl]).x *
+              p.v_scale[head + n];
+        else
+          v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[(head + n) * DH + kl]);
+        if (not_finite(v)) sum += v;
+        int par = p.parent ? p.parent[(size_t)at.b * p.T + n] : n - 1;
+        if (par < -1 || par >= n) par = -1;
+        n = par;
+      }
+      return sum;
+    };
+    // Output of column c (relative to c0) of the item at `at`.
+    auto put = [&](const Cursor& at, int c, float v) {
+      const int node = at.qc * p.tn + (int)col_node[c0 + c];
+      if (c0 + c < p.tn * p.g && node < s_nn[at.b])
+        p.out[(((size_t)at.b * p.T + node) * p.Hq + at.h * p.g + (int)col_head[c0 + c]) * DH + kl] =
+            __float2bfloat16_rn(v);
+    };
+
+    // Writes segment s's result from its O buffer, once its last PV is done: the
+    // output of a whole item, or this CTA's partial of a split one, whose arrival on
+    // fin_full hands it to the finisher.
+    auto finish = [&](int s) {
+      const int sl = s & 1;
+      const int iu = I->seg_u[sl], t0 = I->seg_lo[sl], tl = I->seg_hi[sl];
+      const bool bad = I->seg_bad[sl] != 0;
+      const float unit = FP8 ? exp2f((float)(I->seg_e[sl] - C::kPOff)) : 1.f;  // of O
+      Cursor at;
+      at.init(iu, S);
+      const uint32_t t_o = tmem_o + (uint32_t)(sl * C::kNQP) + lane_off + (uint32_t)c0;
+      const float* sm = seg_m + sl * 64;
+      const float* sls = seg_l + sl * 64;
+      if (t0 == 0 && tl == at.tb - 1) {
+#pragma unroll
+        for (int cc = 0; cc < NQH; cc += 16) {
+          const int w = NQH - cc < 16 ? NQH - cc : 16;
+          float o[16];
+          tmem_ld_chunk(t_o + cc, o, w);
+          tc::tmem_wait_ld();
+          if (kl < DH) {
+#pragma unroll
+            for (int c = 0; c < w; ++c) {
+              float v = FP8 ? o[c] * unit / sls[c0 + cc + c] : o[c] / sls[c0 + cc + c];
+              if (bad) v += unfit(at, c0 + cc + c);
+              put(at, cc + c, v);
+            }
+          }
+        }
+      } else {
+        // slot 0 for the item the range starts in, 1 for the one it ends in
+        const int slot = (iu == item0) ? 0 : 1;
+        float* part = p.partials + ((size_t)cta * 2 + slot) * C::kPartFloats;
+#pragma unroll
+        for (int cc = 0; cc < NQH; cc += 16) {
+          const int w = NQH - cc < 16 ? NQH - cc : 16;
+          float o[16];
+          tmem_ld_chunk(t_o + cc, o, w);
+          tc::tmem_wait_ld();
+          if (kl < DH) {
+            float4* dst = reinterpret_cast<float4*>(part + (size_t)kl * NQ + c0 + cc);
+#pragma unroll
+            for (int v = 0; v < w / 4; ++v)
+              dst[v] = make_float4(o[4 * v] * unit, o[4 * v + 1] * unit, o[4 * v + 2] * unit,
+                                   o[4 * v + 3] * unit);
+          }
+        }
+        if (st < NQ) {
+          part[(size_t)NQ * DH + st] = sm[st];
+          part[(size_t)NQ * DH + NQ + st] = sls[st];
+        }
+        if (st == 0) part[(size_t)NQ * DH + 2 * NQ] = bad ? 1.f : 0.f;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&fin_full[slot]);
+      }
+    };
+
+    // 8 bits: the tile's slot scales, one tile ahead
+    float nks = 0.f, nvs = 0.f;
+    auto load_scales = [&](const Cursor& at) {
+      const int slot = min(at.t * kKT + kl, p.N - 1);
+      const size_t i = ((size_t)at.b * p.Hkv + at.h) * p.N + slot;
+      nks = __ldg(p.k_scale + i);
+      nvs = __ldg(p.v_scale + i);
+    };
+    if constexpr (FP8) load_scales(cs);
+
+    for (int i = 0; i < T; ++i) {
+      const int t = cs.t, qc = cs.qc, b = cs.b;
+      const int len = s_len[b], lim = len + s_nn[b];
+      const bool first = (i == 0 || t == 0);
+      const bool last = (i == T - 1 || t == cs.tb - 1);
+      const bool tree = (t + 1) * kKT > len;  // the tile holds nodes (or slots past them)
+      const int iu = u0 + i - t;              // the item's first unit
+      if (first) {
+        ++seg;
+        seg_t0 = t;
+        e_ref = -1000;
+      }
+      if (tree && b * p.n_qc + qc != anc_key) {
+        // the chunk's nodes' ancestors, a thread a node
+        anc_key = b * p.n_qc + qc;
+        tc::named_bar_sync(1, kSmx);  // nobody reads the old ones any more
+        if (st < p.tn) {
+          uint32_t a[kAncWords];
+#pragma unroll
+          for (int w = 0; w < kAncWords; ++w) a[w] = 0u;
+          int n = qc * p.tn + st;
+          if (n < s_nn[b]) {
+            if (p.parent) {
+              const int32_t* par = p.parent + (size_t)b * p.T;
+              while (n >= 0) {
+#pragma unroll
+                for (int w = 0; w < kAncWords; ++w)
+                  if (w == (n >> 5)) a[w] |= 1u << (n & 31);
+                int up = par[n];
+                if (up < -1 || up >= n) {
+                  set_status(p.status, FDLLM_ERR_BAD_INDEX);
+                  up = -1;
+                }
+                n = up;
+              }
+            } else {
+#pragma unroll
+              for (int w = 0; w < kAncWords; ++w)
+                a[w] = w < (n >> 5) ? ~0u : (w == (n >> 5) ? ~0u >> (31 - (n & 31)) : 0u);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < kAncWords; ++w) anc[st * kAncWords + w] = a[w];
+        }
+        tc::named_bar_sync(1, kSmx);
+      }
+      float ksc = p.qk_scale, vs = 1.f;
+      if constexpr (FP8) {
+        ksc *= nks;
+        vs = nvs;
+      }
+      Cursor cn = cs;
+      if (i + 1 < T) {
+        cn.next(S);
+        if constexpr (FP8) load_scales(cn);
+      }
+      const uint32_t t_oc = tmem_o + (uint32_t)((seg & 1) * C::kNQP);  // this segment's O
+
+      // ---- scores of this tile: row kl of S^T, this thread's columns
+      const int sb = i & 1;
+      // after a timeout every later wait returns at once: keep going, so that all
+      // softmax threads still meet at the same named barriers
+      tc::mbar_wait(&s_full[sb], (uint32_t)(i >> 1) & 1u, abort_flag, p.status);
+      tc::tc_fence_after();
+      float s[NQH];
+#pragma unroll
+      for (int c = 0; c < NQH; c += 16)
+        tmem_ld_chunk(tmem + lane_off + sb * C::kNQP + c0 + c, s + c, NQH - c < 16 ? NQH - c : 16);
+      tc::tmem_wait_ld();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&s_empty[sb]);
+
+      // s becomes the score in log2 units
+      if constexpr (FP8) {
+        const float4* qs4 = reinterpret_cast<const float4*>(qsc + (seg & 1) * 64 + c0);
+#pragma unroll
+        for (int c = 0; c < NQH; c += 4) {
+          const float4 f = qs4[c / 4];
+          s[c] *= ksc * f.x;
+          s[c + 1] *= ksc * f.y;
+          s[c + 2] *= ksc * f.z;
+          s[c + 3] *= ksc * f.w;
+        }
+        if (last) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&q_empty[seg & 1]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NQH; ++c) s[c] *= ksc;
+      }
+      const int slot = t * kKT + kl;
+      bool zero_v = false;  // this slot's V goes into no sum
+      if (tree) {
+        const int j = slot - len;
+        if (slot >= lim) {
+          zero_v = true;
+#pragma unroll
+          for (int c = 0; c < NQH; ++c) s[c] = -INFINITY;
+        } else if (j >= 0) {
+          const uint32_t* aw = anc + (j >> 5);
+#pragma unroll
+          for (int c = 0; c < NQH; ++c)
+            if (!((aw[(int)col_node[c0 + c] * kAncWords] >> (j & 31)) & 1u)) s[c] = -INFINITY;
+        }
+      }
+
+      // ---- running maximum: raised when a score exceeds it by more than 2^kThresh
+      // (masked scores never do); a segment's first tile sets it
+      bool need = first;
+#pragma unroll
+      for (int c = 0; c < NQH; ++c) need |= s[c] - mrun[c] > C::kThresh;
+      int vexp = -1000;
+      if constexpr (FP8) {
+        // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1), at least 2^-100;
+        // scales of slots that go into no sum, zero ones and those that are not finite
+        // do not count
+        const int eb = (__float_as_int(vs) >> 23) & 255;
+        if (!zero_v && eb > 0 && eb < 255) vexp = max(eb - 127, -100);
+        need |= vexp > e_ref;
+      }
+      const bool any = bar_any(2, kSmx, need);
+      if (any) {
+        if (first && st == 0) I->seg_bad[seg & 1] = 0;  // every thread is past finish(seg - 2)
+#pragma unroll
+        for (int c = 0; c < NQH; ++c) {
+          const float wm = warp_max(s[c]);
+          if (lane == (c & 31)) wred[quarter * 64 + c0 + c] = wm;
+        }
+        if constexpr (FP8) {
+          const int e = __reduce_max_sync(0xffffffffu, vexp);
+          if (lane == 0) I->vexp[warp - 2] = e;
+        }
+        tc::named_bar_sync(1, kSmx);
+        int e_new = e_ref;
+        float e_scale = 1.f;
+        if constexpr (FP8) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) e_new = max(e_new, I->vexp[w]);
+          // 2^(e_ref - e_new): 0 from the start value
+          e_scale = e_ref - e_new < -126 ? 0.f : __int_as_float((e_ref - e_new + 127) << 23);
+          e_ref = e_new;
+        }
+        if (st < NQ) {
+          const float mo = first ? kNone : m_run[st];
+          const float tm = fmaxf(fmaxf(wred[st], wred[64 + st]), fmaxf(wred[128 + st], wred[192 + st]));
+          const float mn = (tm - mo > C::kThresh) ? tm : mo;
+          const float al = exp2f(mo - mn);
+          alpha[st] = al;
+          alpha_o[st] = al * e_scale;
+          m_run[st] = mn;
+        }
+        tc::named_bar_sync(1, kSmx);
+#pragma unroll
+        for (int c = 0; c < NQH; ++c) {
+          mrun[c] = m_run[c0 + c];
+          l[c] *= alpha[c0 + c];
+        }
+      }
+
+      // ---- P buffer i&1 is free once PV(i-2) is done; rescaling O needs PV(i-1)
+      if (i >= 2 && pv_waited < i - 2) {
+        tc::mbar_wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1) & 1u, abort_flag, p.status);
+        pv_waited = i - 2;
+      }
+      if (any && !first && pv_waited < i - 1) {
+        tc::mbar_wait(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, abort_flag, p.status);
+        pv_waited = i - 1;
+      }
+      tc::tc_fence_after();
+      if (any && !first) {
+        float o[16];
+#pragma unroll
+        for (int cc = 0; cc < NQH; cc += 16) {
+          const int w = NQH - cc < 16 ? NQH - cc : 16;
+          tmem_ld_chunk(t_oc + lane_off + c0 + cc, o, w);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < w; ++c) o[c] *= alpha_o[c0 + cc + c];
+          tmem_st_chunk(t_oc + lane_off + c0 + cc, o, w);
+        }
+        tc::tmem_wait_st();
+      }
+      if (tree && slot >= len && half == 0) {
+        // V of a slot past the nodes: zeros; of a node: zeros in place of what is not finite
+        tc::mbar_wait(&v_full[i % NV], (uint32_t)(i / NV) & 1u, abort_flag, p.status);
+        uint8_t* row = v_ring + (i % NV) * C::kTileBytes + kl * C::kBoxRow;
+        bool bad = FP8 && !zero_v && not_finite(vs);
+#pragma unroll
+        for (int x = 0; x < C::kBoxes; ++x) {
+#pragma unroll
+          for (int q = 0; q < (int)C::kBoxRow / 16; ++q) {
+            uint4* at = reinterpret_cast<uint4*>(row + x * C::kBoxBytes + q * 16);
+            if (zero_v) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint32_t w[4] = {at->x, at->y, at->z, at->w};
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t m = 0u;  // ones where an element is not finite
+              if constexpr (FP8) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if (((w[e] >> (8 * y)) & 0x7fu) == 0x7fu) m |= 0xffu << (8 * y);
+              } else {
+                if ((w[e] & 0x7f80u) == 0x7f80u) m |= 0xffffu;
+                if ((w[e] & 0x7f800000u) == 0x7f800000u) m |= 0xffff0000u;
+              }
+              if (m) hit = true;
+              w[e] &= ~m;
+            }
+            if (hit) {
+              *at = make_uint4(w[0], w[1], w[2], w[3]);
+              bad = true;
+            }
+          }
+        }
+        if (bad) I->seg_bad[seg & 1] = 1;
+      }
+
+      // ---- P = 2^(s - m) into row kl of the MN-major swizzled P^T tile
+      uint8_t* pb = p_buf + (i & 1) * C::kPBuf;
+      if constexpr (FP8) {
+        // the weight carries the slot's scale against 2^e_ref, times 2^kPOff
+        float w = 0.f;
+        if (!zero_v && !(tree && slot >= len && not_finite(vs)))
+          w = vs * __int_as_float((127 + min(C::kPOff - e_ref, 127)) << 23);
+        uint32_t pk[3][NQH / 4];
+#pragma unroll
+        for (int c = 0; c < NQH; c += 4) {
+          uint32_t hp[2][3];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float p0 = ex2_approx(s[c + 2 * y] - mrun[c + 2 * y]);
+            const float p1 = ex2_approx(s[c + 2 * y + 1] - mrun[c + 2 * y + 1]);
+            l[c + 2 * y] += p0;
+            l[c + 2 * y + 1] += p1;
+            // fp16 value h; its upper byte is e5m2, cut off: h = hi + rest, twice; the
+            // last part is rounded
+            const uint32_t h = pack_f16x2(p0 * w, p1 * w);
+            const uint32_t h1 = h & 0xff00ff00u;
+            const uint32_t r1 = sub_f16x2(h, h1);
+            const uint32_t h2 = r1 & 0xff00ff00u;
+            const uint32_t r2 = sub_f16x2(r1, h2);
+            hp[y][0] = h1;
+            hp[y][1] = h2;
+            hp[y][2] = e5m2x2_of_f16x2(r2);
+          }
+          pk[0][c / 4] = __byte_perm(hp[0][0], hp[1][0], 0x7531);
+          pk[1][c / 4] = __byte_perm(hp[0][1], hp[1][1], 0x7531);
+          pk[2][c / 4] = __byte_perm(hp[0][2], hp[1][2], 0x5410);
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int ch = 0; ch < NQH / 16; ++ch)
+            *reinterpret_cast<uint4*>(pb + part * C::kPPart +
+                                      swz((uint32_t)(kl * C::kPRow + c0 + ch * 16), C::kPRow)) =
+                make_uint4(pk[part][ch * 4], pk[part][ch * 4 + 1], pk[part][ch * 4 + 2],
+                           pk[part][ch * 4 + 3]);
+      } else {
+        uint32_t pk[NQH / 2];
+#pragma unroll
+        for (int c = 0; c < NQH; c += 2) {
+          const float p0 = ex2_approx(s[c] - mrun[c]);
+          const float p1 = ex2_approx(s[c + 1] - mrun[c + 1]);
+          l[c] += p0;
+          l[c + 1] += p1;
+          pk[c / 2] = pack_bf16x2(p0, p1);
+        }
+#pragma unroll
+        for (int ch = 0; ch < NQH / 8; ++ch)
+          *reinterpret_cast<uint4*>(pb + swz((uint32_t)(kl * C::kPRow + c0 * 2 + ch * 16), C::kPRow)) =
+              make_uint4(pk[ch * 4], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
+      }
+      tc::fence_proxy_async_smem();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&p_full[i & 1]);
+
+      if (last) {
+        // ---- segment done: l summed per column; (m, l) are kept for its finish
+#pragma unroll
+        for (int c = 0; c < NQH; ++c) {
+          float v = l[c];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == (c & 31)) wred[quarter * 64 + c0 + c] = v;
+          l[c] = 0.f;
+          mrun[c] = kNone;
+        }
+        tc::named_bar_sync(1, kSmx);
+        const int sl = seg & 1;
+        if (st < NQ) {
+          seg_m[sl * 64 + st] = m_run[st];
+          seg_l[sl * 64 + st] = wred[st] + wred[64 + st] + wred[128 + st] + wred[192 + st];
+        }
+        if (st == 0) {
+          I->seg_u[sl] = iu;
+          I->seg_lo[sl] = seg_t0;
+          I->seg_hi[sl] = t;
+          I->seg_e[sl] = e_ref;
+        }
+        if (sl) end1 = i; else end0 = i;
+        ++n_done;
+      }
+
+      // ---- a finished segment writes its result once its last PV is two tiles back,
+      // and at the latest at the end of the segment after it (the one two on reuses its
+      // O buffer)
+      while (n_fin < n_done) {
+        const int e = (n_fin & 1) ? end1 : end0;
+        if (!(e <= i - 2 || (last && seg == n_fin + 1))) break;
+        if (pv_waited < e) {
+          tc::mbar_wait(&pv_done[e & 1], (uint32_t)(e >> 1) & 1u, abort_flag, p.status);
+          pv_waited = e;
+        }
+        tc::tc_fence_after();
+        finish(n_fin);
+        ++n_fin;
+      }
+      cs = cn;
+    }
+
+    // ---- the segments not yet finished: the last one or two
+    tc::named_bar_sync(1, kSmx);  // their (m, l) and places are in shared memory
+    if (n_fin < n_done) {
+      if (pv_waited < T - 1) {
+        tc::mbar_wait(&pv_done[(T - 1) & 1], (uint32_t)((T - 1) >> 1) & 1u, abort_flag, p.status);
+        pv_waited = T - 1;
+      }
+      tc::tc_fence_after();
+    }
+    while (n_fin < n_done) {
+      finish(n_fin);
+      ++n_fin;
+    }
+    // the finisher has taken the counts of this CTA's partials
+    tc::named_bar_sync(3, kSmx + 32);
+    for (int slot = 0; slot < 2; ++slot) {
+      const int iu = I->merge_u[slot];
+      if (iu < 0) continue;
+      // ---- merge an item whose contributors have all stored their partials, in CTA
+      // order: per column M = max m_j and L = sum 2^(m_j - M) l_j, then
+      // O = sum (2^(m_j - M) / L) O_j with the weights in shared memory
+      __threadfence();
+      Cursor at;
+      at.init(iu, S);
+      const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + at.tb - 1, U, G);
+      const int n_c = c_last - c_first + 1;
+      // the item is slot 0 of a contributor whose range starts inside it
+      auto part_of = [&](int cb) -> const float* {
+        const int sl = (long long)U * cb >= (long long)iu * G ? 0 : 1;
+        return p.partials + ((size_t)cb * 2 + sl) * C::kPartFloats;
+      };
+      float M = kNone, L = 0.f;
+      float mv[8];
+      bool bad = false;
+      for (int j = st; j < n_c; j += kSmx)
+        bad |= __ldcg(part_of(c_first + j) + (size_t)NQ * DH + 2 * NQ) != 0.f;
+      bad = bar_any(2, kSmx, bad);
+      if (st < NQ) {
+        for (int g0 = 0; g0 < n_c; g0 += 8) {
+          float lv[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            mv[j] = kNone;
+            lv[j] = 0.f;
+            if (g0 + j < n_c) {
+              const float* pc = part_of(c_first + g0 + j);
+              mv[j] = __ldcg(pc + (size_t)NQ * DH + st);
+              lv[j] = __ldcg(pc + (size_t)NQ * DH + NQ + st);
+            }
+          }
+          float mc = M;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mc = fmaxf(mc, mv[j]);
+          L *= exp2f(M - mc);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) L += exp2f(mv[j] - mc) * lv[j];
+          M = mc;
+        }
+      }
+      constexpr int kJ = NQH >= 24 ? 2 : 4;  // contributors per batch of O loads
+      float acc[NQH];
+#pragma unroll
+      for (int c = 0; c < NQH; ++c) acc[c] = 0.f;
+      for (int g0 = 0; g0 < n_c; g0 += 8) {
+        if (st < NQ) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float m = mv[j];
+            if (n_c > 8)
+              m = (g0 + j < n_c) ? __ldcg(part_of(c_first + g0 + j) + (size_t)NQ * DH + st) : kNone;
+            wts[j * 64 + st] = exp2f(m - M) / L;
+          }
+        }
+        tc::named_bar_sync(1, kSmx);
+        if (kl < DH) {
+          const int nj = min(8, n_c - g0);
+          for (int j0 = 0; j0 < nj; j0 += kJ) {
+            float4 ov[kJ][NQH / 4];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+              if (j0 + j < nj) {
+                const float4* src = reinterpret_cast<const float4*>(
+                    part_of(c_first + g0 + j0 + j) + (size_t)kl * NQ + c0);
+#pragma unroll
+                for (int v = 0; v < NQH / 4; ++v) ov[j][v] = __ldcg(src + v);
+              }
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+              if (j0 + j < nj) {
+                const float* wj = wts + (j0 + j) * 64 + c0;
+#pragma unroll
+                for (int v = 0; v < NQH / 4; ++v) {
+                  acc[4 * v] = fmaf(wj[4 * v], ov[j][v].x, acc[4 * v]);
+                  acc[4 * v + 1] = fmaf(wj[4 * v + 1], ov[j][v].y, acc[4 * v + 1]);
+                  acc[4 * v + 2] = fmaf(wj[4 * v + 2], ov[j][v].z, acc[4 * v + 2]);
+                  acc[4 * v + 3] = fmaf(wj[4 * v + 3], ov[j][v].w, acc[4 * v + 3]);
+                }
+              }
+          }
+        }
+        tc::named_bar_sync(1, kSmx);
+      }
+      if (kl < DH) {
+#pragma unroll
+        for (int c = 0; c < NQH; ++c) {
+          if (bad) acc[c] += unfit(at, c0 + c);
+          put(at, c, acc[c]);
+        }
+      }
+    }
+  } else if (warp == C::kFinisher) {
+    // ------------------------------------------------------------ finisher
+    // For each partial of this CTA: wait until the softmax warps have issued its
+    // stores, make them visible device-wide, count this contributor in.  The last of
+    // an item's contributors merges it, after its range.
+    if (lane == 0) {
+      I->merge_u[0] = -1;
+      I->merge_u[1] = -1;
+      Cursor ca, cz;
+      ca.init(u0, S);
+      cz.init(u1 - 1, S);
+      for (int slot = 0; slot < 2; ++slot) {
+        const int iu = slot == 0 ? u0 - ca.t : u1 - 1 - cz.t;
+        const int tb = slot == 0 ? ca.tb : cz.tb;
+        if (slot == 1 && iu == u0 - ca.t) break;
+        if (u0 <= iu && u1 >= iu + tb) continue;  // whole: the softmax warps write it
+        bool ready = false;
+        IdleClock clk;
+        while (!(ready = tc::mbar_test(&fin_full[slot], 0u))) {
+          __nanosleep(256);
+          if (!clk.idle(abort_flag, p.status)) break;
+        }
+        if (!ready) break;
+        __threadfence();
+        const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + tb - 1, U, G);
+        // an item that goes on behind CTA c_first's range is the only one to do so, so
+        // c_first names its counter
+        const unsigned prev = atomicAdd(&p.cnt[c_first], 1u);
+        if (prev == (unsigned)(c_last - c_first)) {
+          p.cnt[c_first] = 0u;  // for the next call
+          I->merge_u[slot] = iu;
+        }
+      }
+    }
+    __syncwarp();
+    tc::named_bar_sync(3, kSmx + 32);
+  } else if constexpr (FP8) {
+    // ------------------------------------------------------------ Q splitter
+    // The next item's rows as two e4m3 parts, into the Q buffer its QKs will read.
+    Cursor cq;
+    cq.init(u0, S);
+    int left = T;
+    constexpr int E = DH / 32;  // elements of a lane
+    for (int n = 0; left > 0; ++n) {
+      const int qb = n & 1;
+      tc::mbar_wait(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status);
+      uint8_t* dst = q_buf + qb * C::kQParts * C::kQPart;
+      const int nn = s_nn[cq.b];
+      const int rows = p.tn * p.g;
+      for (int r0 = 0; r0 < NQ; r0 += 8) {
+        uint32_t raw[8][E / 2];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int r = r0 + x;
+          const int node = cq.qc * p.tn + (int)col_node[r];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) raw[x][e] = 0u;
+          if (r < rows && node < nn) {
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                static_cast<const __nv_bfloat16*>(p.q) +
+                (((size_t)cq.b * p.T + node) * p.Hq + cq.h * p.g + (int)col_head[r]) * DH) +
+                lane * (E / 2);
+            if constexpr (E == 4) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src);
+              raw[x][0] = v.x;
+              raw[x][E / 2 - 1] = v.y;
+            } else {
+              raw[x][0] = *src;
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int r = r0 + x;
+          float f[E];
+          uint32_t mx = 0u;  // largest finite |q|, as bits
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            f[e] = __uint_as_float((e & 1) ? raw[x][e / 2] & 0xffff0000u : raw[x][e / 2] << 16);
+            const uint32_t a = __float_as_uint(f[e]) & 0x7fffffffu;
+            if (a < 0x7f800000u) mx = max(mx, a);
+          }
+          mx = __reduce_max_sync(0xffffffffu, mx);
+          // 2^sh takes the largest into [128, 256); q and 2^sh stay normal
+          int sh = 7 - ((int)(mx >> 23) - 127);
+          sh = mx == 0u ? 0 : min(max(sh, -120), 120);
+          const float up = __int_as_float((127 + sh) << 23);
+          uint32_t b1 = 0u, b2 = 0u;
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            float y0 = f[e] * up, y1 = f[e + 1] * up;
+            // what is not finite makes the row NaN (the conversion would saturate it)
+            if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
+            if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
+            const uint32_t q1 = e4m3x2(y0, y1);
+            const float2 g1 = from_e4m3x2(q1);
+            const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
+            b1 |= q1 << (8 * e);
+            b2 |= q2 << (8 * e);
+          }
+          const uint32_t off = swz((uint32_t)(r * DH + lane * E), DH);
+          if constexpr (E == 4) {
+            *reinterpret_cast<uint32_t*>(dst + off) = b1;
+            *reinterpret_cast<uint32_t*>(dst + C::kQPart + off) = b2;
+          } else {
+            *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)b1;
+            *reinterpret_cast<uint16_t*>(dst + C::kQPart + off) = (uint16_t)b2;
+          }
+          if (lane == 0) qsc[qb * 64 + r] = __int_as_float((127 - sh) << 23);
+        }
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full[qb]);
+      left -= cq.tb - cq.t;
+      if (left > 0) cq.next_item(S);
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tc::tmem_dealloc(tmem, ncols);
+  }
+}
+
+struct TreePlan {
+  int NQ, tn, n_qc, nk, nv, grid;
+  size_t smem_bytes;
+};
+
+// Rows of an item: the smallest instance that takes them all, else chunks of 64 (of
+// whole nodes).  A 16-column P of one byte has no swizzled layout, and 24 columns a
+// thread no whole 16-byte chunks: 8 bits run at 32 and 64.
+TreePlan plan(const TreeAttnArgs& a, int num_sms) {
+  TreePlan q{};
+  const int g = a.Hq / a.Hkv, rows = a.T * g;
+  if (a.fp8)
+    q.NQ = rows <= 32 ? 32 : 64;
+  else
+    q.NQ = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 48 ? 48 : 64));
+  q.tn = q.NQ / g < a.T ? q.NQ / g : a.T;
+  q.n_qc = (a.T + q.tn - 1) / q.tn;
+  const long long units = (long long)a.B * a.Hkv * q.n_qc * ((a.N + kKT - 1) / kKT);
+  q.grid = (int)(units < num_sms ? units : num_sms);
+  const size_t boxes = a.fp8 ? 1 : a.dh / 64, elt = a.fp8 ? 1 : 2;
+  const size_t tile = (size_t)kKT * a.dh * elt;
+  const size_t nqp = q.NQ == 48 ? 64 : q.NQ;
+  size_t qbytes = a.fp8 ? (size_t)4 * q.NQ * a.dh : boxes * q.NQ * 128;
+  qbytes = align_up(qbytes, 1024);
+  const size_t pbytes = 2 * (a.fp8 ? 3 : 1) * kKT * nqp * elt;
+  const size_t misc = align_up((size_t)Misc::kSeq + (3 * (size_t)a.B + 1) * 4, 16);
+  const size_t fixed = 1024 + qbytes + pbytes + misc;
+  int tiles = (int)((kSmemBudget - fixed) / tile);
+  if (tiles > 16) tiles = 16;
+  // a V tile is held longer than a K tile: V gets the odd one
+  q.nv = (tiles + 1) / 2;
+  q.nk = tiles - q.nv;
+  q.smem_bytes = fixed + (size_t)tiles * tile;
+  return q;
+}
+
+size_t part_floats(int NQ, int dh) { return (size_t)NQ * dh + 2 * NQ + 4; }
+
+template <int NQ, int DH, bool FP8>
+cudaError_t launch_t(const TreePlan& q, TreeParams prm, const CUtensorMap* maps,
+                     cudaStream_t stream) {
+  using C = Cfg<NQ, DH, FP8>;
+  auto kern = tree_tc_kernel<NQ, DH, FP8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)q.smem_bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(q.grid);
+  cfg.blockDim = dim3(C::kAll);
+  cfg.dynamicSmemBytes = q.smem_bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], prm);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace
+
+size_t tree_tc_workspace_bytes(int Hq, int Hkv, int dh, int T, int num_sms) {
+  // the larger of the two cache forms
+  const int rows = T * (Hq / Hkv);
+  const int NQ = rows <= 32 ? 32 : (rows <= 48 ? 48 : 64);
+  const int NQ8 = rows <= 32 ? 32 : 64;
+  const size_t floats = part_floats(NQ > NQ8 ? NQ : NQ8, dh);
+  return kMaxGrid * sizeof(unsigned) + align_up((size_t)num_sms * 2 * floats * sizeof(float), 256);
+}
+
+cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms > kMaxGrid) return cudaErrorInvalidValue;
+  const TreePlan q = plan(a, sms);
+  if (q.nk < 2 || q.nv < 2) return cudaErrorInvalidValue;
+  if (tree_tc_workspace_bytes(a.Hq, a.Hkv, a.dh, a.T, sms) > a.ws_bytes) return cudaErrorInvalidValue;
+  const uint64_t dh = a.dh, g = a.Hq / a.Hkv;
+  CUtensorMap maps[3];
+  if (!a.fp8) {
+    // q [B, T, Hkv, g, dh]: box {64 dh, g heads, 1 kv head, tn nodes, 1 sequence}
+    const uint64_t dims[5] = {dh, g, (uint64_t)a.Hkv, (uint64_t)a.T, (uint64_t)a.B};
+    const uint64_t strides[4] = {dh * 2, g * dh * 2, (uint64_t)a.Hq * dh * 2,
+                                 (uint64_t)a.T * a.Hq * dh * 2};
+    const uint32_t box[5] = {64, (uint32_t)g, 1, (uint32_t)q.tn, 1};
+    if (!encode_bf16_map(&maps[0], 5, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
+      return cudaErrorInvalidValue;
+  }
+  const void* src[2] = {a.k_cache, a.v_cache};
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t elt = a.fp8 ? 1 : 2;
+    const uint64_t dims[3] = {dh, (uint64_t)a.N, (uint64_t)a.B * a.Hkv};
+    const uint64_t strides[2] = {dh * elt, (uint64_t)a.N * dh * elt};
+    const uint32_t box[3] = {a.fp8 ? (uint32_t)a.dh : 64, kKT, 1};
+    const bool ok =
+        a.fp8 ? encode_u8_map(&maps[1 + i], 3, src[i], dims, strides, box,
+                              a.dh == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+              : encode_bf16_map(&maps[1 + i], 3, src[i], dims, strides, box,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  if (a.fp8) maps[0] = maps[1];  // not read
+  TreeParams prm{};
+  prm.B = a.B; prm.N = a.N; prm.Hq = a.Hq; prm.Hkv = a.Hkv; prm.g = (int)g; prm.T = a.T;
+  prm.n_qc = q.n_qc; prm.tn = q.tn; prm.nk = q.nk; prm.nv = q.nv;
+  prm.keep = q.n_qc > 1;
+  prm.qk_scale = kLog2e / sqrtf((float)a.dh);
+  prm.q = a.q; prm.v_cache = a.v_cache; prm.k_scale = a.k_scale; prm.v_scale = a.v_scale;
+  prm.cache_len = a.cache_len; prm.parent = a.parent; prm.n_nodes = a.n_nodes;
+  prm.out = static_cast<__nv_bfloat16*>(a.out);
+  prm.status = a.status;
+  prm.cnt = static_cast<unsigned*>(a.ws);
+  prm.partials = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kMaxGrid * sizeof(unsigned));
+#define FDLLM_TREE_CASE(NQv, DHv, FP8v) \
+  if (q.NQ == NQv && a.dh == DHv && (a.fp8 != 0) == FP8v) return launch_t<NQv, DHv, FP8v>(q, prm, maps, stream);
+  FDLLM_TREE_CASE(16, 64, false)
+  FDLLM_TREE_CASE(32, 64, false)
+  FDLLM_TREE_CASE(48, 64, false)
+  FDLLM_TREE_CASE(64, 64, false)
+  FDLLM_TREE_CASE(16, 128, false)
+  FDLLM_TREE_CASE(32, 128, false)
+  FDLLM_TREE_CASE(48, 128, false)
+  FDLLM_TREE_CASE(64, 128, false)
+  FDLLM_TREE_CASE(32, 64, true)
+  FDLLM_TREE_CASE(64, 64, true)
+  FDLLM_TREE_CASE(32, 128, true)
+  FDLLM_TREE_CASE(64, 128, true)
+#undef FDLLM_TREE_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fdllm
