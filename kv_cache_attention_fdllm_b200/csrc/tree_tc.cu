@@ -88,7 +88,7 @@ struct TreeParams {
 
 template <int NQ, int DH, bool FP8>
 struct Cfg {
-  static constexpr int kCols = NQ == 64 ? 32 : (NQ == 48 ? 24 : 16);  // rows of a softmax thread
+  static constexpr int kCols = 16;  // rows of a softmax thread
   static constexpr int kSmx = 128 * NQ / kCols;
   static constexpr int kFinisher = 2 + kSmx / 32;  // warp index
   static constexpr int kAll = 64 + kSmx + 32 + (FP8 ? 32 : 0);
@@ -106,24 +106,25 @@ struct Cfg {
   static constexpr uint32_t kPPart = kKT * kPRow;          // a multiple of 1024
   static constexpr uint32_t kPBuf = kPParts * kPPart;
   // largest exponent step a weight may exceed the running maximum's by, and the
-  // power of two weights are kept at (8 bits: below 2^(2+12+1) in fp16 and e5m2)
-  static constexpr float kThresh = FP8 ? 2.f : 8.f;
-  static constexpr int kPOff = FP8 ? 12 : 0;
+  // power of two weights are kept at (8 bits: below 2^(6+8+1) in fp16 and e5m2).  A
+  // larger step would rescale less often but leave less room below
+  static constexpr float kThresh = FP8 ? 6.f : 8.f;
+  static constexpr int kPOff = FP8 ? 8 : 0;
   static constexpr int kPartFloats = NQ * DH + 2 * NQ + 4;  // O, m, l, flag (and padding)
 };
 
 // Shared memory behind the tiles (byte offsets of the misc block).
 struct Misc {
   static constexpr int kBars = 0;        // 46 mbarriers
-  static constexpr int kInts = 384;      // see Ints
+  static constexpr int kInts = 384;      // Ints (128 bytes)
   static constexpr int kM = 512;         // m_run[64], alpha[64], alpha_o[64]
   static constexpr int kRed = 1280;      // wred[4][64]
   static constexpr int kSegM = 2304;     // seg_m[2][64], seg_l[2][64]
-  static constexpr int kNode = 3328;     // col_node[64], col_head[64] (bytes)
-  static constexpr int kQsc = 3456;      // qsc[2][64]
-  static constexpr int kAnc = 3968;      // anc[64][kAncWords]
-  static constexpr int kWts = kAnc + 64 * kAncWords * 4;  // [8][64] merge weights
-  static constexpr int kSeq = kWts + 8 * 64 * 4;          // pre[B + 1], len[B], nn[B]
+  static constexpr int kCol = 3328;      // col_node[64] (bytes), col_off[64] (ints)
+  static constexpr int kQsc = 3648;      // qsc[2][64]
+  static constexpr int kPar = 4160;      // parents of a sequence's nodes [kMaxNodes]
+  static constexpr int kAnc = kPar + kMaxNodes * 4;       // anc[64][kAncWords]
+  static constexpr int kSeq = kAnc + 64 * kAncWords * 4;  // pre[B + 1], len[B], nn[B]
 };
 
 struct Ints {
@@ -131,11 +132,12 @@ struct Ints {
   int abort;
   int merge_u[2];    // first unit of the item in partial slot s that this CTA merges, or -1
   int seg_u[2];      // a finished segment (by O buffer): its item's first unit,
-  int seg_lo[2];     // its first tile,
-  int seg_hi[2];     // its last,
+  int seg_at[2];     // chunk | whole << 30, sequence, kv head of its item,
+  int seg_b[2];
+  int seg_h[2];
   int seg_bad[2];    // whether it met a node's V that is not finite,
   int seg_e[2];      // and the power of two its weights were taken against
-  int vexp[8];       // exponents of the softmax warps' V scales
+  int vexp[4];       // exponents of the V scales of a quarter's slots
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -189,11 +191,6 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
 // e4m3 of two floats (lo in the low byte) and the floats they stand for
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -209,11 +206,149 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
       : "r"(h));
   return f;
 }
+// a load that stays where it is written (the compiler moves plain ones down to their use,
+// and the wait for memory with them)
+__device__ __forceinline__ float ld_early(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
 // byte offset `off` of a tile whose rows have `row` bytes (32, 64 or 128), swizzled
 __device__ __forceinline__ uint32_t swz(uint32_t off, uint32_t row) {
   return off ^ (((off >> 7) & (row / 16 - 1)) << 4);
 }
 __device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.4028234663852886e38f); }
+
+// Adds to out[dh row d] of the item's rows [c0, c1) the values of their visible nodes' V
+// that are not finite (they were left out of the products).  Kept out of line, like all
+// that is rare: code that is not in the instruction cache costs microseconds to fetch.
+template <int DH, bool FP8>
+__device__ __noinline__ void add_unfit(const TreeParams& p, int qc, int b, int h, int len, int nn,
+                                       int c0, int c1, int d) {
+  const size_t head = ((size_t)b * p.Hkv + h) * p.N + len;
+  const int32_t* parent = p.parent ? p.parent + (size_t)b * p.T : nullptr;
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+    const int node = qc * p.tn + c / p.g;
+    if (c >= p.tn * p.g || node >= nn) return;
+    float sum = 0.f;
+    bool any = false;
+#pragma unroll 1
+    for (int n = node; n >= 0;) {
+      float v;
+      if constexpr (FP8)
+        v = from_e4m3x2(static_cast<const uint8_t*>(p.v_cache)[(head + n) * DH + d]).x *
+            p.v_scale[head + n];
+      else
+        v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[(head + n) * DH + d]);
+      if (not_finite(v)) {
+        sum += v;
+        any = true;
+      }
+      int up = parent ? parent[n] : n - 1;
+      if (up < -1 || up >= n) up = -1;
+      n = up;
+    }
+    if (any) {
+      __nv_bfloat16* o = p.out + (((size_t)b * p.T + node) * p.Hq + h * p.g + c % p.g) * DH + d;
+      *o = __float2bfloat16_rn(__bfloat162float(*o) + sum);
+    }
+  }
+}
+
+// Rows r0, r0 + step, .. of a chunk's Q (bf16) as two e4m3 parts: q 2^sh = q1 + q2 with
+// the row's largest in [128, 256); 2^-sh into qsc[row].  Rows past the sequence's nodes
+// become zeros.  A warp a row.
+template <int NQ, int DH>
+__device__ __noinline__ void split_q(const TreeParams& p, int qc, int b, int h, int nn, int r0,
+                                     int step, uint8_t* dst, float* qsc) {
+  constexpr int E = DH / 32;  // elements of a lane
+  constexpr int kBatch = 4;   // rows whose loads are in flight together
+  constexpr uint32_t kPart = NQ * DH;
+  const int lane = threadIdx.x & 31;
+  const int rows = p.tn * p.g;
+#pragma unroll 1
+  for (int r1 = r0; r1 < NQ; r1 += kBatch * step) {
+    uint2 raw[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int r = r1 + x * step;
+      raw[x] = make_uint2(0u, 0u);
+      const int node = qc * p.tn + r / p.g;
+      if (r < rows && node < nn) {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                   (((size_t)b * p.T + node) * p.Hq + h * p.g + r % p.g) * DH +
+                                   lane * E;
+        if constexpr (E == 4)
+          raw[x] = *reinterpret_cast<const uint2*>(src);
+        else
+          raw[x].x = *reinterpret_cast<const uint32_t*>(src);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int r = r1 + x * step;
+      float f[E];
+      uint32_t mx = 0u;  // largest finite |q|, as bits
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t w = e < 2 ? raw[x].x : raw[x].y;
+        f[e] = __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
+        const uint32_t a = __float_as_uint(f[e]) & 0x7fffffffu;
+        if (a < 0x7f800000u) mx = max(mx, a);
+      }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      int sh = 7 - ((int)(mx >> 23) - 127);
+      sh = mx == 0u ? 0 : min(max(sh, -120), 120);
+      const float up = __int_as_float((127 + sh) << 23);
+      uint32_t b1 = 0u, b2 = 0u;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        float y0 = f[e] * up, y1 = f[e + 1] * up;
+        // what is not finite makes the row NaN (the conversion would saturate it)
+        if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
+        if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
+        const uint32_t q1 = e4m3x2(y0, y1);
+        const float2 g1 = from_e4m3x2(q1);
+        const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
+        b1 |= q1 << (8 * e);
+        b2 |= q2 << (8 * e);
+      }
+      if (r < NQ) {
+        const uint32_t off = swz((uint32_t)(r * DH + lane * E), DH);
+        if constexpr (E == 4) {
+          *reinterpret_cast<uint32_t*>(dst + off) = b1;
+          *reinterpret_cast<uint32_t*>(dst + kPart + off) = b2;
+        } else {
+          *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)b1;
+          *reinterpret_cast<uint16_t*>(dst + kPart + off) = (uint16_t)b2;
+        }
+        if (lane == 0) qsc[r] = __int_as_float((127 - sh) << 23);
+      }
+    }
+  }
+}
+
+// A node's row of V in shared memory (boxes of `row` bytes, `box` bytes apart): zeros in
+// place of elements that are not finite; whether there were any.
+template <bool FP8>
+__device__ __noinline__ void zero_unfit(uint8_t* at, int row, int boxes, int box) {
+#pragma unroll 1
+  for (int x = 0; x < boxes; ++x)
+#pragma unroll 1
+    for (int q = 0; q < row / 4; ++q) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(at + x * box) + q;
+      uint32_t m = 0u;
+      if constexpr (FP8) {
+        for (int y = 0; y < 32; y += 8)
+          if (((*w >> y) & 0x7fu) == 0x7fu) m |= 0xffu << y;
+      } else {
+        for (int y = 0; y < 32; y += 16)
+          if (((*w >> y) & 0x7f80u) == 0x7f80u) m |= 0xffffu << y;
+      }
+      if (m) *w &= ~m;
+    }
+}
 
 // Polling loops give up after kWaitLimitNs without progress.
 struct IdleClock {
@@ -324,11 +459,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   float* wred = reinterpret_cast<float*>(misc + Misc::kRed);  // [4][64]
   float* seg_m = reinterpret_cast<float*>(misc + Misc::kSegM);
   float* seg_l = seg_m + 2 * 64;
-  uint8_t* col_node = misc + Misc::kNode;
-  uint8_t* col_head = col_node + 64;
+  uint8_t* col_node = misc + Misc::kCol;
+  int* col_off = reinterpret_cast<int*>(misc + Misc::kCol + 64);  // of a row in out
   float* qsc = reinterpret_cast<float*>(misc + Misc::kQsc);  // [2][64]
+  int* s_par = reinterpret_cast<int*>(misc + Misc::kPar);
   uint32_t* anc = reinterpret_cast<uint32_t*>(misc + Misc::kAnc);
-  float* wts = reinterpret_cast<float*>(misc + Misc::kWts);
   int* s_pre = reinterpret_cast<int*>(misc + Misc::kSeq);
   int* s_len = s_pre + p.B + 1;
   int* s_nn = s_len + p.B;
@@ -359,8 +494,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   }
   if (warp == 1) tc::tmem_alloc(&I->tmem, ncols);
   if (tid < 64) {
-    col_node[tid] = (uint8_t)(tid / p.g);
-    col_head[tid] = (uint8_t)(tid % p.g);
+    const int n = tid / p.g;
+    col_node[tid] = (uint8_t)n;
+    col_off[tid] = (n * p.Hq + tid - n * p.g) * DH;
   }
   // rows of Q past the chunk's: zeros, whatever the product makes of them is not read
   for (int i = tid; i < (int)(C::kQBytes / 16); i += C::kAll)
@@ -599,50 +735,26 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     cs.init(u0, S);
     const int item0 = u0 - cs.t;  // first unit of the item the range starts in
 
-    // Sum of the values of column c's visible nodes that are not finite, at dh row kl
-    // (0 without any): re-read from the cache, for the rare item that has some.
-    auto unfit = [&](const Cursor& at, int c) -> float {
-      float sum = 0.f;
-      const int len = s_len[at.b], nn = s_nn[at.b];
-      int n = at.qc * p.tn + (int)col_node[c];
-      if (n >= nn) return 0.f;
-      const size_t head = ((size_t)at.b * p.Hkv + at.h) * p.N + len;
-      while (n >= 0) {
-        float v;
-        if constexpr (FP8)
-          v = from_e4m3x2(static_cast<const uint8_t*>(p.v_cache)[(head + n) * DH + kl]).x *
-              p.v_scale[head + n];
-        else
-          v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[(head + n) * DH + kl]);
-        if (not_finite(v)) sum += v;
-        int par = p.parent ? p.parent[(size_t)at.b * p.T + n] : n - 1;
-        if (par < -1 || par >= n) par = -1;
-        n = par;
-      }
-      return sum;
+    // Where the item's rows go in out, and how many columns are rows of the sequence.
+    auto out_of = [&](int qc, int b, int h) {
+      return p.out + (((size_t)b * p.T + qc * p.tn) * p.Hq + h * p.g) * DH + kl;
     };
-    // Output of column c (relative to c0) of the item at `at`.
-    auto put = [&](const Cursor& at, int c, float v) {
-      const int node = at.qc * p.tn + (int)col_node[c0 + c];
-      if (c0 + c < p.tn * p.g && node < s_nn[at.b])
-        p.out[(((size_t)at.b * p.T + node) * p.Hq + at.h * p.g + (int)col_head[c0 + c]) * DH + kl] =
-            __float2bfloat16_rn(v);
-    };
+    auto columns = [&](int qc, int b) { return min(p.tn, s_nn[b] - qc * p.tn) * p.g; };
 
     // Writes segment s's result from its O buffer, once its last PV is done: the
     // output of a whole item, or this CTA's partial of a split one, whose arrival on
     // fin_full hands it to the finisher.
     auto finish = [&](int s) {
       const int sl = s & 1;
-      const int iu = I->seg_u[sl], t0 = I->seg_lo[sl], tl = I->seg_hi[sl];
-      const bool bad = I->seg_bad[sl] != 0;
+      const int qc = I->seg_at[sl] & 0x3fffffff, b = I->seg_b[sl], h = I->seg_h[sl];
       const float unit = FP8 ? exp2f((float)(I->seg_e[sl] - C::kPOff)) : 1.f;  // of O
-      Cursor at;
-      at.init(iu, S);
       const uint32_t t_o = tmem_o + (uint32_t)(sl * C::kNQP) + lane_off + (uint32_t)c0;
       const float* sm = seg_m + sl * 64;
       const float* sls = seg_l + sl * 64;
-      if (t0 == 0 && tl == at.tb - 1) {
+      const bool bad = I->seg_bad[sl] != 0;
+      if (I->seg_at[sl] >> 30) {
+        __nv_bfloat16* o_at = out_of(qc, b, h);
+        const int ncol = columns(qc, b);
 #pragma unroll
         for (int cc = 0; cc < NQH; cc += 16) {
           const int w = NQH - cc < 16 ? NQH - cc : 16;
@@ -651,16 +763,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           tc::tmem_wait_ld();
           if (kl < DH) {
 #pragma unroll
-            for (int c = 0; c < w; ++c) {
-              float v = FP8 ? o[c] * unit / sls[c0 + cc + c] : o[c] / sls[c0 + cc + c];
-              if (bad) v += unfit(at, c0 + cc + c);
-              put(at, cc + c, v);
-            }
+            for (int c = 0; c < w; ++c)
+              if (c0 + cc + c < ncol)
+                o_at[col_off[c0 + cc + c]] =
+                    __float2bfloat16_rn(__fdividef(o[c] * unit, sls[c0 + cc + c]));
           }
         }
+        if (bad && kl < DH) add_unfit<DH, FP8>(p, qc, b, h, s_len[b], s_nn[b], c0, c0 + NQH, kl);
       } else {
         // slot 0 for the item the range starts in, 1 for the one it ends in
-        const int slot = (iu == item0) ? 0 : 1;
+        const int slot = (I->seg_u[sl] == item0) ? 0 : 1;
         float* part = p.partials + ((size_t)cta * 2 + slot) * C::kPartFloats;
 #pragma unroll
         for (int cc = 0; cc < NQH; cc += 16) {
@@ -669,10 +781,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           tmem_ld_chunk(t_o + cc, o, w);
           tc::tmem_wait_ld();
           if (kl < DH) {
-            float4* dst = reinterpret_cast<float4*>(part + (size_t)kl * NQ + c0 + cc);
+            // O as [NQ / 4][dh row][4]: a warp's 16-byte accesses are consecutive
+            float4* dst = reinterpret_cast<float4*>(part) + (c0 + cc) / 4 * DH + kl;
 #pragma unroll
             for (int v = 0; v < w / 4; ++v)
-              dst[v] = make_float4(o[4 * v] * unit, o[4 * v + 1] * unit, o[4 * v + 2] * unit,
+              dst[v * DH] = make_float4(o[4 * v] * unit, o[4 * v + 1] * unit, o[4 * v + 2] * unit,
                                    o[4 * v + 3] * unit);
           }
         }
@@ -688,17 +801,26 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
     // 8 bits: the tile's slot scales, one tile ahead
     float nks = 0.f, nvs = 0.f;
-    auto load_scales = [&](const Cursor& at) {
-      const int slot = min(at.t * kKT + kl, p.N - 1);
-      const size_t i = ((size_t)at.b * p.Hkv + at.h) * p.N + slot;
-      nks = __ldg(p.k_scale + i);
-      nvs = __ldg(p.v_scale + i);
+    size_t sc_head = 0;  // the head's first scale
+    auto load_scales = [&](int t) {
+      const size_t i = sc_head + min(t * kKT + kl, p.N - 1);
+      nks = ld_early(p.k_scale + i);
+      nvs = ld_early(p.v_scale + i);
     };
-    if constexpr (FP8) load_scales(cs);
+    auto head_of = [&](const Cursor& at) { return ((size_t)at.b * p.Hkv + at.h) * p.N; };
+    if constexpr (FP8) {
+      sc_head = head_of(cs);
+      load_scales(cs.t);
+      // the range's first Q is split by all of these warps: nothing else is to do yet
+      split_q<NQ, DH>(p, cs.qc, cs.b, cs.h, s_nn[cs.b], warp - 2, kSmx / 32, q_buf, qsc);
+      tc::fence_proxy_async_smem();
+      tc::named_bar_sync(1, kSmx);
+      if (st == 0) tc::mbar_arrive(&q_full[0]);
+    }
 
+    int len = s_len[cs.b], lim = len + s_nn[cs.b];
     for (int i = 0; i < T; ++i) {
       const int t = cs.t, qc = cs.qc, b = cs.b;
-      const int len = s_len[b], lim = len + s_nn[b];
       const bool first = (i == 0 || t == 0);
       const bool last = (i == T - 1 || t == cs.tb - 1);
       const bool tree = (t + 1) * kKT > len;  // the tile holds nodes (or slots past them)
@@ -712,33 +834,28 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // the chunk's nodes' ancestors, a thread a node
         anc_key = b * p.n_qc + qc;
         tc::named_bar_sync(1, kSmx);  // nobody reads the old ones any more
-        if (st < p.tn) {
-          uint32_t a[kAncWords];
-#pragma unroll
-          for (int w = 0; w < kAncWords; ++w) a[w] = 0u;
-          int n = qc * p.tn + st;
-          if (n < s_nn[b]) {
-            if (p.parent) {
-              const int32_t* par = p.parent + (size_t)b * p.T;
-              while (n >= 0) {
-#pragma unroll
-                for (int w = 0; w < kAncWords; ++w)
-                  if (w == (n >> 5)) a[w] |= 1u << (n & 31);
-                int up = par[n];
-                if (up < -1 || up >= n) {
-                  set_status(p.status, FDLLM_ERR_BAD_INDEX);
-                  up = -1;
-                }
-                n = up;
+        if (p.parent)
+          for (int n = st; n < s_nn[b]; n += kSmx) s_par[n] = p.parent[(size_t)b * p.T + n];
+        for (int w = st; w < p.tn * kAncWords; w += kSmx) anc[w] = 0u;
+        tc::named_bar_sync(1, kSmx);
+        int n = qc * p.tn + st;
+        if (st < p.tn && n < s_nn[b]) {
+          uint32_t* a = anc + st * kAncWords;
+          if (p.parent) {
+#pragma unroll 1
+            while (n >= 0) {
+              a[n >> 5] |= 1u << (n & 31);
+              int up = s_par[n];
+              if (up < -1 || up >= n) {
+                set_status(p.status, FDLLM_ERR_BAD_INDEX);
+                up = -1;
               }
-            } else {
-#pragma unroll
-              for (int w = 0; w < kAncWords; ++w)
-                a[w] = w < (n >> 5) ? ~0u : (w == (n >> 5) ? ~0u >> (31 - (n & 31)) : 0u);
+              n = up;
             }
+          } else {
+#pragma unroll 1
+            for (int w = 0; w <= n >> 5; ++w) a[w] = w < (n >> 5) ? ~0u : ~0u >> (31 - (n & 31));
           }
-#pragma unroll
-          for (int w = 0; w < kAncWords; ++w) anc[st * kAncWords + w] = a[w];
         }
         tc::named_bar_sync(1, kSmx);
       }
@@ -747,10 +864,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         ksc *= nks;
         vs = nvs;
       }
-      Cursor cn = cs;
-      if (i + 1 < T) {
-        cn.next(S);
-        if constexpr (FP8) load_scales(cn);
+      if constexpr (FP8) {
+        if (!last) load_scales(t + 1);
       }
       const uint32_t t_oc = tmem_o + (uint32_t)((seg & 1) * C::kNQP);  // this segment's O
 
@@ -806,9 +921,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
       // ---- running maximum: raised when a score exceeds it by more than 2^kThresh
       // (masked scores never do); a segment's first tile sets it
-      bool need = first;
+      float d[NQH];  // exponents of the weights
+      float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < NQH; ++c) need |= s[c] - mrun[c] > C::kThresh;
+      for (int c = 0; c < NQH; ++c) {
+        d[c] = s[c] - mrun[c];
+        top = fmaxf(top, d[c]);
+      }
+      bool need = first || top > C::kThresh;
       int vexp = -1000;
       if constexpr (FP8) {
         // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1), at least 2^-100;
@@ -828,7 +948,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if constexpr (FP8) {
           const int e = __reduce_max_sync(0xffffffffu, vexp);
-          if (lane == 0) I->vexp[warp - 2] = e;
+          if (lane == 0 && half == 0) I->vexp[quarter] = e;
         }
         tc::named_bar_sync(1, kSmx);
         int e_new = e_ref;
@@ -853,6 +973,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
         for (int c = 0; c < NQH; ++c) {
           mrun[c] = m_run[c0 + c];
+          d[c] = s[c] - mrun[c];
           l[c] *= alpha[c0 + c];
         }
       }
@@ -884,39 +1005,30 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // V of a slot past the nodes: zeros; of a node: zeros in place of what is not finite
         tc::mbar_wait(&v_full[i % NV], (uint32_t)(i / NV) & 1u, abort_flag, p.status);
         uint8_t* row = v_ring + (i % NV) * C::kTileBytes + kl * C::kBoxRow;
-        bool bad = FP8 && !zero_v && not_finite(vs);
-#pragma unroll
-        for (int x = 0; x < C::kBoxes; ++x) {
-#pragma unroll
-          for (int q = 0; q < (int)C::kBoxRow / 16; ++q) {
-            uint4* at = reinterpret_cast<uint4*>(row + x * C::kBoxBytes + q * 16);
-            if (zero_v) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            uint32_t w[4] = {at->x, at->y, at->z, at->w};
-            bool hit = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t m = 0u;  // ones where an element is not finite
-              if constexpr (FP8) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  if (((w[e] >> (8 * y)) & 0x7fu) == 0x7fu) m |= 0xffu << (8 * y);
-              } else {
-                if ((w[e] & 0x7f80u) == 0x7f80u) m |= 0xffffu;
-                if ((w[e] & 0x7f800000u) == 0x7f800000u) m |= 0xffff0000u;
-              }
-              if (m) hit = true;
-              w[e] &= ~m;
-            }
-            if (hit) {
-              *at = make_uint4(w[0], w[1], w[2], w[3]);
-              bad = true;
-            }
+        if (zero_v) {
+#pragma unroll 2
+          for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
+            const int x = q / (C::kBoxRow / 16);
+            *reinterpret_cast<uint4*>(row + x * C::kBoxBytes + (q - x * (C::kBoxRow / 16)) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
           }
+        } else {
+          // an exponent of all ones (an e4m3 of all ones) carries into the sign's place
+          constexpr uint32_t ones = FP8 ? 0x7f7f7f7fu : 0x7f807f80u;
+          constexpr uint32_t one = FP8 ? 0x01010101u : 0x00800080u;
+          constexpr uint32_t sign = FP8 ? 0x80808080u : 0x80008000u;
+          uint32_t hit = 0u;
+#pragma unroll 4
+          for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
+            const int x = q / (C::kBoxRow / 16);
+            const uint4 w = *reinterpret_cast<const uint4*>(row + x * C::kBoxBytes +
+                                                            (q - x * (C::kBoxRow / 16)) * 16);
+            hit |= ((w.x & ones) + one) | ((w.y & ones) + one) | ((w.z & ones) + one) |
+                   ((w.w & ones) + one);
+          }
+          if ((hit & sign) != 0u) zero_unfit<FP8>(row, C::kBoxRow, C::kBoxes, C::kBoxBytes);
+          if ((hit & sign) != 0u || (FP8 && not_finite(vs))) I->seg_bad[seg & 1] = 1;
         }
-        if (bad) I->seg_bad[seg & 1] = 1;
       }
 
       // ---- P = 2^(s - m) into row kl of the MN-major swizzled P^T tile
@@ -932,12 +1044,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           uint32_t hp[2][3];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float p0 = ex2_approx(s[c + 2 * y] - mrun[c + 2 * y]);
-            const float p1 = ex2_approx(s[c + 2 * y + 1] - mrun[c + 2 * y + 1]);
+            const float p0 = ex2_approx(d[c + 2 * y]);
+            const float p1 = ex2_approx(d[c + 2 * y + 1]);
             l[c + 2 * y] += p0;
             l[c + 2 * y + 1] += p1;
             // fp16 value h; its upper byte is e5m2, cut off: h = hi + rest, twice; the
-            // last part is rounded
+            // last part is rounded (half a unit added below the byte; it never carries
+            // past 16 bits, parts being far below the largest)
             const uint32_t h = pack_f16x2(p0 * w, p1 * w);
             const uint32_t h1 = h & 0xff00ff00u;
             const uint32_t r1 = sub_f16x2(h, h1);
@@ -945,11 +1058,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const uint32_t r2 = sub_f16x2(r1, h2);
             hp[y][0] = h1;
             hp[y][1] = h2;
-            hp[y][2] = e5m2x2_of_f16x2(r2);
+            hp[y][2] = r2 + 0x00800080u;
           }
           pk[0][c / 4] = __byte_perm(hp[0][0], hp[1][0], 0x7531);
           pk[1][c / 4] = __byte_perm(hp[0][1], hp[1][1], 0x7531);
-          pk[2][c / 4] = __byte_perm(hp[0][2], hp[1][2], 0x5410);
+          pk[2][c / 4] = __byte_perm(hp[0][2], hp[1][2], 0x7531);
         }
 #pragma unroll
         for (int part = 0; part < 3; ++part)
@@ -963,8 +1076,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         uint32_t pk[NQH / 2];
 #pragma unroll
         for (int c = 0; c < NQH; c += 2) {
-          const float p0 = ex2_approx(s[c] - mrun[c]);
-          const float p1 = ex2_approx(s[c + 1] - mrun[c + 1]);
+          const float p0 = ex2_approx(d[c]);
+          const float p1 = ex2_approx(d[c + 1]);
           l[c] += p0;
           l[c + 1] += p1;
           pk[c / 2] = pack_bf16x2(p0, p1);
@@ -998,8 +1111,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if (st == 0) {
           I->seg_u[sl] = iu;
-          I->seg_lo[sl] = seg_t0;
-          I->seg_hi[sl] = t;
+          I->seg_at[sl] = qc | ((seg_t0 == 0 && t == cs.tb - 1) ? 1 << 30 : 0);
+          I->seg_b[sl] = b;
+          I->seg_h[sl] = cs.h;
           I->seg_e[sl] = e_ref;
         }
         if (sl) end1 = i; else end0 = i;
@@ -1020,7 +1134,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         finish(n_fin);
         ++n_fin;
       }
-      cs = cn;
+      if (!last) {
+        ++cs.t;
+      } else if (i + 1 < T) {
+        cs.next_item(S);
+        len = s_len[cs.b];
+        lim = len + s_nn[cs.b];
+        if constexpr (FP8) {
+          sc_head = head_of(cs);
+          load_scales(0);
+        }
+      }
     }
 
     // ---- the segments not yet finished: the last one or two
@@ -1043,94 +1167,80 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (iu < 0) continue;
       // ---- merge an item whose contributors have all stored their partials, in CTA
       // order: per column M = max m_j and L = sum 2^(m_j - M) l_j, then
-      // O = sum (2^(m_j - M) / L) O_j with the weights in shared memory
+      // O = sum (2^(m_j - M) / L) O_j.  The tiles' shared memory is idle by now and takes
+      // the contributors' m and weights; every round of loads is issued whole before its
+      // first use.
       __threadfence();
       Cursor at;
       at.init(iu, S);
       const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + at.tb - 1, U, G);
       const int n_c = c_last - c_first + 1;
       // the item is slot 0 of a contributor whose range starts inside it
-      auto part_of = [&](int cb) -> const float* {
-        const int sl = (long long)U * cb >= (long long)iu * G ? 0 : 1;
+      const long long iu_g = (long long)iu * G;
+      auto part_of = [&](int j) -> const float* {
+        const int cb = c_first + j;
+        const int sl = (long long)U * cb < iu_g;
         return p.partials + ((size_t)cb * 2 + sl) * C::kPartFloats;
       };
-      float M = kNone, L = 0.f;
-      float mv[8];
+      float* w_m = reinterpret_cast<float*>(smem);  // [n_c][NQ]: m, then the weights
+      float* w_l = w_m + n_c * NQ;                  // [n_c][NQ]
       bool bad = false;
-      for (int j = st; j < n_c; j += kSmx)
-        bad |= __ldcg(part_of(c_first + j) + (size_t)NQ * DH + 2 * NQ) != 0.f;
+#pragma unroll 4
+      for (int x = st; x < n_c * NQ; x += kSmx) {
+        const int j = x / NQ, c = x - j * NQ;
+        const float* pc = part_of(j) + (size_t)NQ * DH;
+        w_m[x] = __ldcg(pc + c);
+        w_l[x] = __ldcg(pc + NQ + c);
+        if (c == 0) bad |= __ldcg(pc + 2 * NQ) != 0.f;
+      }
       bad = bar_any(2, kSmx, bad);
       if (st < NQ) {
-        for (int g0 = 0; g0 < n_c; g0 += 8) {
-          float lv[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            mv[j] = kNone;
-            lv[j] = 0.f;
-            if (g0 + j < n_c) {
-              const float* pc = part_of(c_first + g0 + j);
-              mv[j] = __ldcg(pc + (size_t)NQ * DH + st);
-              lv[j] = __ldcg(pc + (size_t)NQ * DH + NQ + st);
-            }
-          }
-          float mc = M;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) mc = fmaxf(mc, mv[j]);
-          L *= exp2f(M - mc);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) L += exp2f(mv[j] - mc) * lv[j];
-          M = mc;
-        }
+        float M = kNone, L = 0.f;
+        for (int j = 0; j < n_c; ++j) M = fmaxf(M, w_m[j * NQ + st]);
+        for (int j = 0; j < n_c; ++j) L += exp2f(w_m[j * NQ + st] - M) * w_l[j * NQ + st];
+        const float inv = 1.f / L;
+        for (int j = 0; j < n_c; ++j) w_m[j * NQ + st] = exp2f(w_m[j * NQ + st] - M) * inv;
       }
-      constexpr int kJ = NQH >= 24 ? 2 : 4;  // contributors per batch of O loads
+      tc::named_bar_sync(1, kSmx);
       float acc[NQH];
 #pragma unroll
       for (int c = 0; c < NQH; ++c) acc[c] = 0.f;
-      for (int g0 = 0; g0 < n_c; g0 += 8) {
-        if (st < NQ) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float m = mv[j];
-            if (n_c > 8)
-              m = (g0 + j < n_c) ? __ldcg(part_of(c_first + g0 + j) + (size_t)NQ * DH + st) : kNone;
-            wts[j * 64 + st] = exp2f(m - M) / L;
-          }
-        }
-        tc::named_bar_sync(1, kSmx);
-        if (kl < DH) {
-          const int nj = min(8, n_c - g0);
-          for (int j0 = 0; j0 < nj; j0 += kJ) {
-            float4 ov[kJ][NQH / 4];
-#pragma unroll
-            for (int j = 0; j < kJ; ++j)
-              if (j0 + j < nj) {
-                const float4* src = reinterpret_cast<const float4*>(
-                    part_of(c_first + g0 + j0 + j) + (size_t)kl * NQ + c0);
-#pragma unroll
-                for (int v = 0; v < NQH / 4; ++v) ov[j][v] = __ldcg(src + v);
-              }
-#pragma unroll
-            for (int j = 0; j < kJ; ++j)
-              if (j0 + j < nj) {
-                const float* wj = wts + (j0 + j) * 64 + c0;
-#pragma unroll
-                for (int v = 0; v < NQH / 4; ++v) {
-                  acc[4 * v] = fmaf(wj[4 * v], ov[j][v].x, acc[4 * v]);
-                  acc[4 * v + 1] = fmaf(wj[4 * v + 1], ov[j][v].y, acc[4 * v + 1]);
-                  acc[4 * v + 2] = fmaf(wj[4 * v + 2], ov[j][v].z, acc[4 * v + 2]);
-                  acc[4 * v + 3] = fmaf(wj[4 * v + 3], ov[j][v].w, acc[4 * v + 3]);
-                }
-              }
-          }
-        }
-        tc::named_bar_sync(1, kSmx);
-      }
       if (kl < DH) {
+        constexpr int kJ = 4;  // contributors per round of loads
+        for (int j0 = 0; j0 < n_c; j0 += kJ) {
+          float4 ov[kJ][NQH / 4];
 #pragma unroll
-        for (int c = 0; c < NQH; ++c) {
-          if (bad) acc[c] += unfit(at, c0 + c);
-          put(at, c, acc[c]);
+          for (int j = 0; j < kJ; ++j) {
+            // past the last contributor: its values once more, not used
+            const float4* src = reinterpret_cast<const float4*>(part_of(min(j0 + j, n_c - 1))) +
+                                c0 / 4 * DH + kl;
+#pragma unroll
+            for (int v = 0; v < NQH / 4; ++v) ov[j][v] = __ldcg(src + v * DH);
+          }
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            if (j0 + j >= n_c) break;
+            const float4* wj = reinterpret_cast<const float4*>(w_m + (j0 + j) * NQ + c0);
+#pragma unroll
+            for (int v = 0; v < NQH / 4; ++v) {
+              const float4 w = wj[v];
+              acc[4 * v] = fmaf(w.x, ov[j][v].x, acc[4 * v]);
+              acc[4 * v + 1] = fmaf(w.y, ov[j][v].y, acc[4 * v + 1]);
+              acc[4 * v + 2] = fmaf(w.z, ov[j][v].z, acc[4 * v + 2]);
+              acc[4 * v + 3] = fmaf(w.w, ov[j][v].w, acc[4 * v + 3]);
+            }
+          }
         }
+      }
+      tc::named_bar_sync(1, kSmx);  // the weights are read: the next item may take their place
+      if (kl < DH) {
+        __nv_bfloat16* o_at = out_of(at.qc, at.b, at.h);
+        const int ncol = columns(at.qc, at.b);
+#pragma unroll
+        for (int c = 0; c < NQH; ++c)
+          if (c0 + c < ncol) o_at[col_off[c0 + c]] = __float2bfloat16_rn(acc[c]);
+        if (bad)
+          add_unfit<DH, FP8>(p, at.qc, at.b, at.h, s_len[at.b], s_nn[at.b], c0, c0 + NQH, kl);
       }
     }
   } else if (warp == C::kFinisher) {
@@ -1172,83 +1282,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   } else if constexpr (FP8) {
     // ------------------------------------------------------------ Q splitter
     // The next item's rows as two e4m3 parts, into the Q buffer its QKs will read.
+    // (the first is split by the softmax warps)
     Cursor cq;
     cq.init(u0, S);
-    int left = T;
-    constexpr int E = DH / 32;  // elements of a lane
-    for (int n = 0; left > 0; ++n) {
+    int left = T - (cq.tb - cq.t);
+    for (int n = 1; left > 0; ++n) {
       const int qb = n & 1;
+      cq.next_item(S);
       tc::mbar_wait(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status);
-      uint8_t* dst = q_buf + qb * C::kQParts * C::kQPart;
-      const int nn = s_nn[cq.b];
-      const int rows = p.tn * p.g;
-      for (int r0 = 0; r0 < NQ; r0 += 8) {
-        uint32_t raw[8][E / 2];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int r = r0 + x;
-          const int node = cq.qc * p.tn + (int)col_node[r];
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) raw[x][e] = 0u;
-          if (r < rows && node < nn) {
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                static_cast<const __nv_bfloat16*>(p.q) +
-                (((size_t)cq.b * p.T + node) * p.Hq + cq.h * p.g + (int)col_head[r]) * DH) +
-                lane * (E / 2);
-            if constexpr (E == 4) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              raw[x][0] = v.x;
-              raw[x][E / 2 - 1] = v.y;
-            } else {
-              raw[x][0] = *src;
-            }
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int r = r0 + x;
-          float f[E];
-          uint32_t mx = 0u;  // largest finite |q|, as bits
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            f[e] = __uint_as_float((e & 1) ? raw[x][e / 2] & 0xffff0000u : raw[x][e / 2] << 16);
-            const uint32_t a = __float_as_uint(f[e]) & 0x7fffffffu;
-            if (a < 0x7f800000u) mx = max(mx, a);
-          }
-          mx = __reduce_max_sync(0xffffffffu, mx);
-          // 2^sh takes the largest into [128, 256); q and 2^sh stay normal
-          int sh = 7 - ((int)(mx >> 23) - 127);
-          sh = mx == 0u ? 0 : min(max(sh, -120), 120);
-          const float up = __int_as_float((127 + sh) << 23);
-          uint32_t b1 = 0u, b2 = 0u;
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            float y0 = f[e] * up, y1 = f[e + 1] * up;
-            // what is not finite makes the row NaN (the conversion would saturate it)
-            if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
-            if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
-            const uint32_t q1 = e4m3x2(y0, y1);
-            const float2 g1 = from_e4m3x2(q1);
-            const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
-            b1 |= q1 << (8 * e);
-            b2 |= q2 << (8 * e);
-          }
-          const uint32_t off = swz((uint32_t)(r * DH + lane * E), DH);
-          if constexpr (E == 4) {
-            *reinterpret_cast<uint32_t*>(dst + off) = b1;
-            *reinterpret_cast<uint32_t*>(dst + C::kQPart + off) = b2;
-          } else {
-            *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)b1;
-            *reinterpret_cast<uint16_t*>(dst + C::kQPart + off) = (uint16_t)b2;
-          }
-          if (lane == 0) qsc[qb * 64 + r] = __int_as_float((127 - sh) << 23);
-        }
-      }
+      split_q<NQ, DH>(p, cq.qc, cq.b, cq.h, s_nn[cq.b], 0, 1, q_buf + qb * C::kQParts * C::kQPart,
+                      qsc + qb * 64);
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&q_full[qb]);
-      left -= cq.tb - cq.t;
-      if (left > 0) cq.next_item(S);
+      left -= cq.tb;
     }
   }
 
@@ -1294,6 +1341,8 @@ TreePlan plan(const TreeAttnArgs& a, int num_sms) {
   q.nv = (tiles + 1) / 2;
   q.nk = tiles - q.nv;
   q.smem_bytes = fixed + (size_t)tiles * tile;
+  // a merge keeps two floats a row of every contributor where the tiles were
+  if ((size_t)q.grid * q.NQ * 8 > (size_t)tiles * tile) q.grid = (int)(tiles * tile / (q.NQ * 8));
   return q;
 }
 
