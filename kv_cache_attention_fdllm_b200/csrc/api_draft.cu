@@ -28,9 +28,9 @@ fdllm_status check_tree(int B, int N, int Hq, int Hkv, int dh, int T, int dtype)
   if (T > FDLLM_MAX_TREE_NODES || B > FDLLM_MAX_TREE_SEQS || Hq / Hkv > 64 || Hq > 4096)
     return FDLLM_ERR_UNSUPPORTED;
   if ((long long)B * N > (1ll << 31) || N > (1 << 30)) return FDLLM_ERR_UNSUPPORTED;
-  // work units (chunk of at most 64 rows of whole nodes, sequence, kv head, 128 slots)
+  // work units (chunk of at most 32 rows, sequence, kv head, 128 slots)
   // are counted in 32 bits
-  const int g = Hq / Hkv, tn = 64 / g, chunks = (T + tn - 1) / tn;
+  const int g = Hq / Hkv, tn = g < 32 ? 32 / g : 1, chunks = (T + tn - 1) / tn * (g > 32 ? 2 : 1);
   if ((long long)B * Hkv * ((N + 127) / 128) * chunks > (1ll << 30)) return FDLLM_ERR_UNSUPPORTED;
   return FDLLM_OK;
 }

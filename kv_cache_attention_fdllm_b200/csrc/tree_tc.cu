@@ -14,17 +14,17 @@
 // they are, with no conversion pass, because everything else fits around them:
 //   - a slot's scale multiplies one row of S^T, i.e. one thread's scores, and for V
 //     the weights of that thread;
-//   - a bf16 query has 8 significant bits, an e4m3 value 4: q 2^-x = q1 + q2 with both
-//     e4m3 (x per row, so that the row's largest is in [128, 256)) is exact down to
-//     2^-10 against the largest, and S = K q1 + K q2 accumulates in the same place;
+//   - a bf16 query has 8 significant bits, an e4m3 value 4: q 2^x = q1 + q2 with both
+//     e4m3 (x per chunk, so that its largest is in [128, 256)) is exact down to 2^-10,
+//     2^-17 of the largest, and S = K q1 + K q2;
 //   - a weight is taken as three e5m2 parts (3 significant bits each, of its fp16
 //     value): 9 bits, as bf16 has 8, over a range of 2^31, so that a long flat rest
 //     far below a sink keeps its weight.  e4m3 parts would lose it (2^17).  The
 //     weights carry the slot's scale relative to a power of two that follows the
 //     scales as the running maximum follows the scores.
-// The second and third parts cost tensor time, of which there is plenty: a tile
-// takes 20 instructions of 32 cycles (its A operand through shared memory) against
-// some 1400 cycles for its bytes from HBM.
+// The parts are more columns of the same MMAs, and an MMA takes some 80 cycles (its
+// 128 x 32 bytes of A) whatever its columns: a tile's 8 take about half of the 1400
+// cycles that its bytes take from HBM.  (As separate products they took 20.)
 //
 // Work split: persistent stream-K.  Units are laid out chunk by chunk, sequence by
 // sequence, head by head, tile by tile, from the lengths on the device; CTAs take
@@ -36,12 +36,12 @@
 //
 //   warp 0      TMA producer: K and V tiles, and the rows' Q (16-bit cache)
 //   warp 1      TMEM; lane 0 issues both products
-//   warps 2..   softmax (NQ / kCols groups of 4 warps), epilogue, merges
-//   then        finisher: counts the partials in
-//   last        (8-bit) splits the next item's Q into its two e4m3 parts
+//   warp 2      finisher: counts the partials in; 8 bits: splits the next item's Q into
+//               its two e4m3 parts
+//   warps 4..   softmax (one group, or two that take turns at the tiles), epilogue, merges
 //
-// O^T is double-buffered in TMEM: an item's result is written two tiles into the
-// next item, off the softmax path.
+// O^T is double-buffered in TMEM (once for each group): an item's result is written
+// some tiles into the next item, off the softmax path.
 //
 // NaN and infinity.  Slots past the sequence's nodes are masked in S and zeroed in V
 // (0 x NaN would be NaN).  A node's V that is not finite is zeroed the same way, since
@@ -69,7 +69,8 @@ constexpr size_t kSmemBudget = 227 * 1024;
 
 struct TreeParams {
   int B, N, Hq, Hkv, g, T;
-  int n_qc, tn;         // chunks of rows, nodes of a chunk (tn * g rows)
+  int n_qc, tn;         // chunks of rows, nodes of a chunk (tn * gs rows)
+  int gs, hs;           // query heads of a chunk: g, or with hs = 2 chunks to a node half of them
   int nk, nv;           // stages of the K and V rings
   int keep;             // tiles are read by several chunks
   float qk_scale;       // log2(e) / sqrt(dh)
@@ -88,10 +89,18 @@ struct TreeParams {
 
 template <int NQ, int DH, bool FP8>
 struct Cfg {
-  static constexpr int kCols = 16;  // rows of a softmax thread
-  static constexpr int kSmx = 128 * NQ / kCols;
-  static constexpr int kFinisher = 2 + kSmx / 32;  // warp index
-  static constexpr int kAll = 64 + kSmx + 32 + (FP8 ? 32 : 0);
+  // Softmax threads.  Two groups that take turns at the tiles where a tile's way through
+  // one (scores, maximum, weights, each behind a wait) takes longer than its bytes: in 8
+  // bits, and in the latency of the few rows of single tokens (measured at 16 rows, one
+  // sequence: 22.9 us with one group, 20.0 with two).  Else one group with more registers
+  // (32 rows, 64 sequences of 4096: 712 us with two groups, 685 with one).
+  static constexpr int kGroups = (FP8 || NQ <= 16) ? 2 : 1;
+  static constexpr int kCols = 16;  // rows of a thread
+  static constexpr int kGroupThreads = 128 * NQ / kCols;
+  static constexpr int kSmx = kGroups * kGroupThreads;
+  static constexpr int kFinCols = NQ / (kSmx / 128);  // rows of a thread when results are written
+  static constexpr int kFinisher = 2, kFirst = 4;  // warp indices
+  static constexpr int kAll = 32 * kFirst + kSmx;
   static constexpr int kNQP = NQ == 48 ? 64 : NQ;  // columns of a TMEM buffer, of P's layout
   static constexpr int kBoxes = FP8 ? 1 : DH / 64;
   static constexpr uint32_t kBoxRow = FP8 ? DH : 128;  // bytes of a slot in a box
@@ -101,10 +110,13 @@ struct Cfg {
   static constexpr int kQParts = FP8 ? 2 : 1;
   static constexpr uint32_t kQPart = NQ * (FP8 ? DH : DH * 2);
   static constexpr uint32_t kQBytes = (kQBufs * kQParts * kQPart + 1023) / 1024 * 1024;
-  static constexpr int kPParts = FP8 ? 3 : 1;
-  static constexpr uint32_t kPRow = kNQP * (FP8 ? 1 : 2);  // bytes of a slot in P
-  static constexpr uint32_t kPPart = kKT * kPRow;          // a multiple of 1024
-  static constexpr uint32_t kPBuf = kPParts * kPPart;
+  // 8 bits: the parts lie side by side as more columns of one product (an MMA takes some
+  // 80 cycles, its 128 x 32 bytes of A, whatever its columns): S has 2 NQ, P and O 3 NQ
+  static constexpr int kSCols = FP8 ? 2 * NQ : kNQP;
+  static constexpr int kOParts = FP8 ? 3 : 1;
+  static constexpr int kOCols = FP8 ? 3 * NQ : kNQP;
+  static constexpr uint32_t kPRow = FP8 ? 128 : kNQP * 2;  // bytes of a slot in P
+  static constexpr uint32_t kPBuf = kKT * kPRow;           // a multiple of 1024
   // largest exponent step a weight may exceed the running maximum's by, and the
   // power of two weights are kept at (8 bits: below 2^(6+8+1) in fp16 and e5m2).  A
   // larger step would rescale less often but leave less room below
@@ -113,32 +125,42 @@ struct Cfg {
   static constexpr int kPartFloats = NQ * DH + 2 * NQ + 4;  // O, m, l, flag (and padding)
 };
 
-// Shared memory behind the tiles (byte offsets of the misc block).
+// Shared memory: this block, Q, the P buffers, the K ring, the V ring, the sequences'
+// tables, the 8-bit slot scales.  All but the last three are at constant offsets, which
+// spares the softmax threads their addresses.
 struct Misc {
-  static constexpr int kBars = 0;        // 46 mbarriers
-  static constexpr int kInts = 384;      // Ints (128 bytes)
-  static constexpr int kM = 512;         // m_run[64], alpha[64], alpha_o[64]
-  static constexpr int kRed = 1280;      // wred[4][64]
-  static constexpr int kSegM = 2304;     // seg_m[2][64], seg_l[2][64]
-  static constexpr int kCol = 3328;      // col_node[64] (bytes), col_off[64] (ints)
-  static constexpr int kQsc = 3648;      // qsc[2][64]
-  static constexpr int kPar = 4160;      // parents of a sequence's nodes [kMaxNodes]
-  static constexpr int kAnc = kPar + kMaxNodes * 4;       // anc[64][kAncWords]
-  static constexpr int kSeq = kAnc + 64 * kAncWords * 4;  // pre[B + 1], len[B], nn[B]
+  static constexpr int kBars = 0;               // 50 mbarriers
+  static constexpr int kInts = 400;             // Ints
+  static constexpr int kM = 640;                // by group: m_run[64], alpha[64], alpha_o[64]
+  static constexpr int kRed = kM + 2 * 768;     // by group: wred[4][64]
+  static constexpr int kSegM = kRed + 2 * 1024; // seg_m, seg_l [2 O buffers][2 groups][64]
+  static constexpr int kCol = kSegM + 2 * 1024; // col_node[64] (bytes), col_off[64] (ints)
+  static constexpr int kQsc = kCol + 320;       // qsc[2], maxima of Q by warp [16], [2][2]
+  static constexpr int kZero = kQsc + 128;      // [64] zeros
+  static constexpr int kPar = kZero + 256;      // by group: parents of a sequence's nodes
+  static constexpr int kAnc = kPar + 2 * kMaxNodes * 4;       // by group: anc[64][kAncWords]
+  static constexpr int kBytes = (kAnc + 2 * 64 * kAncWords * 4 + 1023) / 1024 * 1024;
+  // of pre[B + 1], len[B], nn[B]
+  __host__ __device__ static constexpr int seq_bytes(int B) { return ((3 * B + 1) * 4 + 15) / 16 * 16; }
 };
 
 struct Ints {
   uint32_t tmem;
   int abort;
-  int merge_u[2];    // first unit of the item in partial slot s that this CTA merges, or -1
-  int seg_u[2];      // a finished segment (by O buffer): its item's first unit,
-  int seg_at[2];     // chunk | whole << 30, sequence, kv head of its item,
-  int seg_b[2];
-  int seg_h[2];
-  int seg_bad[2];    // whether it met a node's V that is not finite,
-  int seg_e[2];      // and the power of two its weights were taken against
-  int vexp[4];       // exponents of the V scales of a quarter's slots
+  int merge_u[2];     // first unit of the item in partial slot s that this CTA merges, or -1
+  // a closed segment, by O buffer and group: has the group tiles in it, the power of two
+  // its weights were taken against, did it meet a node's V that is not finite
+  int seg_has[2][2];
+  int seg_e[2][2];
+  int seg_bad[2][2];
+  int bad_run[2];     // the last of the running segment, by group
+  int vexp[2][4];     // by group: exponents of the V scales of a quarter's slots
+  // the item of a closed segment, by O buffer and group (every thread of the group writes
+  // the same): chunk, sequence, kv head, its first unit, whether the segment is all of it,
+  // and the group's last tile in it
+  int item[2][2][6];
 };
+static_assert(sizeof(Ints) <= 240, "Misc::kM");
 
 __device__ __forceinline__ float warp_max(float v) {
   float r;
@@ -206,12 +228,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
       : "r"(h));
   return f;
 }
-// a load that stays where it is written (the compiler moves plain ones down to their use,
-// and the wait for memory with them)
-__device__ __forceinline__ float ld_early(const float* p) {
-  float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-  return v;
+// one float into shared memory, asynchronously; and the wait for all of the thread's
+__device__ __forceinline__ void copy_async4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 // byte offset `off` of a tile whose rows have `row` bytes (32, 64 or 128), swizzled
 __device__ __forceinline__ uint32_t swz(uint32_t off, uint32_t row) {
@@ -227,10 +250,11 @@ __device__ __noinline__ void add_unfit(const TreeParams& p, int qc, int b, int h
                                        int c0, int c1, int d) {
   const size_t head = ((size_t)b * p.Hkv + h) * p.N + len;
   const int32_t* parent = p.parent ? p.parent + (size_t)b * p.T : nullptr;
+  const int h0 = qc % p.hs * p.gs;  // first of the chunk's heads
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
-    const int node = qc * p.tn + c / p.g;
-    if (c >= p.tn * p.g || node >= nn) return;
+    const int node = qc / p.hs * p.tn + c / p.gs, hd = h0 + c % p.gs;
+    if (c >= p.tn * p.gs || node >= nn || hd >= p.g) return;
     float sum = 0.f;
     bool any = false;
 #pragma unroll 1
@@ -250,83 +274,82 @@ __device__ __noinline__ void add_unfit(const TreeParams& p, int qc, int b, int h
       n = up;
     }
     if (any) {
-      __nv_bfloat16* o = p.out + (((size_t)b * p.T + node) * p.Hq + h * p.g + c % p.g) * DH + d;
+      __nv_bfloat16* o = p.out + (((size_t)b * p.T + node) * p.Hq + h * p.g + hd) * DH + d;
       *o = __float2bfloat16_rn(__bfloat162float(*o) + sum);
     }
   }
 }
 
-// Rows r0, r0 + step, .. of a chunk's Q (bf16) as two e4m3 parts: q 2^sh = q1 + q2 with
-// the row's largest in [128, 256); 2^-sh into qsc[row].  Rows past the sequence's nodes
-// become zeros.  A warp a row.
-template <int NQ, int DH>
-__device__ __noinline__ void split_q(const TreeParams& p, int qc, int b, int h, int nn, int r0,
-                                     int step, uint8_t* dst, float* qsc) {
+// A chunk's Q (bf16) as two e4m3 parts: q 2^sh = q1 + q2 with the chunk's largest in
+// [128, 256), so that what is lost is below 2^-18 of it.  Rows past the sequence's nodes
+// become zeros.  Warp w of W takes every W-th row, all its loads in flight together;
+// `share`: the maximum over the warps.  Returns 2^-sh.
+template <int NQ, int DH, int W, typename Share>
+__device__ __forceinline__ float split_q(const TreeParams& p, int qc, int b, int h, int nn, int w,
+                                         uint8_t* dst, Share share) {
+  constexpr int R = NQ / W;   // rows of a warp
   constexpr int E = DH / 32;  // elements of a lane
-  constexpr int kBatch = 4;   // rows whose loads are in flight together
   constexpr uint32_t kPart = NQ * DH;
   const int lane = threadIdx.x & 31;
-  const int rows = p.tn * p.g;
-#pragma unroll 1
-  for (int r1 = r0; r1 < NQ; r1 += kBatch * step) {
-    uint2 raw[kBatch];
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const int r = r1 + x * step;
-      raw[x] = make_uint2(0u, 0u);
-      const int node = qc * p.tn + r / p.g;
-      if (r < rows && node < nn) {
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                   (((size_t)b * p.T + node) * p.Hq + h * p.g + r % p.g) * DH +
-                                   lane * E;
-        if constexpr (E == 4)
-          raw[x] = *reinterpret_cast<const uint2*>(src);
-        else
-          raw[x].x = *reinterpret_cast<const uint32_t*>(src);
-      }
+  const int rows = p.tn * p.gs, h0 = qc % p.hs * p.gs;
+  auto load = [&](int r) {
+    uint2 raw = make_uint2(0u, 0u);
+    const int node = qc / p.hs * p.tn + r / p.gs, hd = h0 + r % p.gs;
+    if (r < rows && node < nn && hd < p.g) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                 (((size_t)b * p.T + node) * p.Hq + h * p.g + hd) * DH + lane * E;
+      if constexpr (E == 4)
+        raw = *reinterpret_cast<const uint2*>(src);
+      else
+        raw.x = *reinterpret_cast<const uint32_t*>(src);
     }
+    return raw;
+  };
+  // the largest finite |q|, as the upper 16 bits of a float: bf16 magnitudes compare as
+  // whole numbers
+  uint2 raw[R];
 #pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      const int r = r1 + x * step;
-      float f[E];
-      uint32_t mx = 0u;  // largest finite |q|, as bits
+  for (int x = 0; x < R; ++x) raw[x] = load(w + x * W);
+  uint32_t mx = 0u;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t w = e < 2 ? raw[x].x : raw[x].y;
-        f[e] = __uint_as_float((e & 1) ? w & 0xffff0000u : w << 16);
-        const uint32_t a = __float_as_uint(f[e]) & 0x7fffffffu;
-        if (a < 0x7f800000u) mx = max(mx, a);
-      }
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      int sh = 7 - ((int)(mx >> 23) - 127);
-      sh = mx == 0u ? 0 : min(max(sh, -120), 120);
-      const float up = __int_as_float((127 + sh) << 23);
-      uint32_t b1 = 0u, b2 = 0u;
+  for (int x = 0; x < R; ++x) {
+    const uint32_t a[4] = {raw[x].x & 0x7fffu, (raw[x].x >> 16) & 0x7fffu, raw[x].y & 0x7fffu,
+                           (raw[x].y >> 16) & 0x7fffu};
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        float y0 = f[e] * up, y1 = f[e + 1] * up;
-        // what is not finite makes the row NaN (the conversion would saturate it)
-        if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
-        if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
-        const uint32_t q1 = e4m3x2(y0, y1);
-        const float2 g1 = from_e4m3x2(q1);
-        const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
-        b1 |= q1 << (8 * e);
-        b2 |= q2 << (8 * e);
-      }
-      if (r < NQ) {
-        const uint32_t off = swz((uint32_t)(r * DH + lane * E), DH);
-        if constexpr (E == 4) {
-          *reinterpret_cast<uint32_t*>(dst + off) = b1;
-          *reinterpret_cast<uint32_t*>(dst + kPart + off) = b2;
-        } else {
-          *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)b1;
-          *reinterpret_cast<uint16_t*>(dst + kPart + off) = (uint16_t)b2;
-        }
-        if (lane == 0) qsc[r] = __int_as_float((127 - sh) << 23);
-      }
+    for (int e = 0; e < 4; ++e)
+      if (a[e] < 0x7f80u) mx = max(mx, a[e]);
+  }
+  mx = share(__reduce_max_sync(0xffffffffu, mx));
+  int sh = 7 - ((int)(mx >> 7) - 127);
+  sh = mx == 0u ? 0 : min(max(sh, -120), 120);
+  const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+  for (int x = 0; x < R; ++x) {
+    const int r = w + x * W;
+    uint32_t b1 = 0u, b2 = 0u;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const uint32_t q = e < 2 ? raw[x].x : raw[x].y;
+      float y0 = __uint_as_float(q << 16) * up, y1 = __uint_as_float(q & 0xffff0000u) * up;
+      // what is not finite makes the row NaN (the conversion would saturate it)
+      if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
+      if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
+      const uint32_t q1 = e4m3x2(y0, y1);
+      const float2 g1 = from_e4m3x2(q1);
+      const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
+      b1 |= q1 << (8 * e);
+      b2 |= q2 << (8 * e);
+    }
+    const uint32_t off = swz((uint32_t)(r * DH + lane * E), DH);
+    if constexpr (E == 4) {
+      *reinterpret_cast<uint32_t*>(dst + off) = b1;
+      *reinterpret_cast<uint32_t*>(dst + kPart + off) = b2;
+    } else {
+      *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)b1;
+      *reinterpret_cast<uint16_t*>(dst + kPart + off) = (uint16_t)b2;
     }
   }
+  return __int_as_float((127 - sh) << 23);
 }
 
 // A node's row of V in shared memory (boxes of `row` bytes, `box` bytes apart): zeros in
@@ -349,6 +372,9 @@ __device__ __noinline__ void zero_unfit(uint8_t* at, int row, int boxes, int box
       if (m) *w &= ~m;
     }
 }
+
+// orders this thread's view of memory, device-wide, around an atomic count
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
 // Polling loops give up after kWaitLimitNs without progress.
 struct IdleClock {
@@ -435,11 +461,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const int NK = p.nk, NV = p.nv;
-  uint8_t* k_ring = smem;
-  uint8_t* v_ring = smem + NK * C::kTileBytes;
-  uint8_t* q_buf = v_ring + NV * C::kTileBytes;
+  uint8_t* misc = smem;
+  uint8_t* q_buf = smem + Misc::kBytes;
   uint8_t* p_buf = q_buf + C::kQBytes;
-  uint8_t* misc = p_buf + 2 * C::kPBuf;
+  uint8_t* k_ring = p_buf + 2 * C::kPBuf;
+  uint8_t* v_ring = k_ring + NK * C::kTileBytes;
+  int* s_pre = reinterpret_cast<int*>(v_ring + NV * C::kTileBytes);
+  int* s_len = s_pre + p.B + 1;
+  int* s_nn = s_len + p.B;
   uint64_t* k_full = reinterpret_cast<uint64_t*>(misc + Misc::kBars);
   uint64_t* k_empty = k_full + 8;
   uint64_t* v_full = k_empty + 8;
@@ -451,27 +480,28 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   uint64_t* p_full = s_empty + 2;    // [2]
   uint64_t* pv_done = p_full + 2;    // [2]
   uint64_t* fin_full = pv_done + 2;  // [2] a partial's stores are issued
+  uint64_t* seg_full = fin_full + 2; // [2] by O buffer: both groups' O of the segment is final
+  uint64_t* o_empty = seg_full + 2;  // [2] by O buffer: its result is written
   Ints* I = reinterpret_cast<Ints*>(misc + Misc::kInts);
   int* abort_flag = &I->abort;
-  float* m_run = reinterpret_cast<float*>(misc + Misc::kM);
-  float* alpha = m_run + 64;    // rescale of l
-  float* alpha_o = alpha + 64;  // rescale of O
-  float* wred = reinterpret_cast<float*>(misc + Misc::kRed);  // [4][64]
+  float* s_mrun = reinterpret_cast<float*>(misc + Misc::kM);
+  float* s_wred = reinterpret_cast<float*>(misc + Misc::kRed);
   float* seg_m = reinterpret_cast<float*>(misc + Misc::kSegM);
-  float* seg_l = seg_m + 2 * 64;
+  float* seg_l = seg_m + 2 * 128;
   uint8_t* col_node = misc + Misc::kCol;
   int* col_off = reinterpret_cast<int*>(misc + Misc::kCol + 64);  // of a row in out
-  float* qsc = reinterpret_cast<float*>(misc + Misc::kQsc);  // [2][64]
+  float* qsc = reinterpret_cast<float*>(misc + Misc::kQsc);  // [2], then the first split's maxima
+  float* s_zero = reinterpret_cast<float*>(misc + Misc::kZero);  // [64] zeros
   int* s_par = reinterpret_cast<int*>(misc + Misc::kPar);
-  uint32_t* anc = reinterpret_cast<uint32_t*>(misc + Misc::kAnc);
-  int* s_pre = reinterpret_cast<int*>(misc + Misc::kSeq);
-  int* s_len = s_pre + p.B + 1;
-  int* s_nn = s_len + p.B;
+  uint32_t* s_anc = reinterpret_cast<uint32_t*>(misc + Misc::kAnc);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
-  constexpr uint32_t ncols = 4 * C::kNQP < 32 ? 32 : 4 * C::kNQP;  // 64, 128 or 256
+  // two S and two O a group
+  constexpr uint32_t cols = 2 * C::kSCols + 2 * C::kGroups * C::kOCols;
+  constexpr uint32_t ncols = cols <= 128 ? 128 : (cols <= 256 ? 256 : 512);
+  static_assert(cols <= 512, "TMEM");
 
   if (tid == 0) {
     for (int s = 0; s < 8; ++s) {
@@ -481,22 +511,26 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       tc::mbar_init(&v_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(&q_full[b], 1);
+      tc::mbar_init(&q_full[b], FP8 ? 2 : 1);  // 8 bits: the two warps that split Q
       tc::mbar_init(&q_empty[b], 1 + (FP8 ? kSmx / 32 : 0));  // 8 bits: the scales' readers too
       tc::mbar_init(&s_full[b], 1);
-      tc::mbar_init(&s_empty[b], kSmx / 32);
-      tc::mbar_init(&p_full[b], kSmx / 32);
+      tc::mbar_init(&s_empty[b], C::kGroupThreads / 32);
+      tc::mbar_init(&p_full[b], C::kGroupThreads / 32);
+      tc::mbar_init(&seg_full[b], kSmx / 32);
+      tc::mbar_init(&o_empty[b], kSmx / 32);
       tc::mbar_init(&pv_done[b], 1);
       tc::mbar_init(&fin_full[b], kSmx / 32);
     }
     I->abort = 0;
+    I->bad_run[0] = I->bad_run[1] = 0;
     tc::fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(&I->tmem, ncols);
   if (tid < 64) {
-    const int n = tid / p.g;
+    s_zero[tid] = 0.f;
+    const int n = tid / p.gs;
     col_node[tid] = (uint8_t)n;
-    col_off[tid] = (n * p.Hq + tid - n * p.g) * DH;
+    col_off[tid] = (n * p.Hq + tid - n * p.gs) * DH;
   }
   // rows of Q past the chunk's: zeros, whatever the product makes of them is not read
   for (int i = tid; i < (int)(C::kQBytes / 16); i += C::kAll)
@@ -540,7 +574,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = I->tmem;
-  const uint32_t tmem_o = tmem + 2 * C::kNQP;
+  const uint32_t tmem_o = tmem + 2 * C::kSCols;
   Seqs S;
   S.pre = s_pre;
   S.B = p.B;
@@ -615,562 +649,648 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // Two in-order streams, QK(i) and PV(j), each issued as soon as its inputs are
-    // ready.
-    if (lane == 0) {
-      constexpr uint32_t swz_code = C::kBoxRow == 128 ? 2u : 4u;
-      constexpr uint32_t p_swz = C::kPRow == 128 ? 2u : (C::kPRow == 64 ? 4u : 6u);
-      const uint32_t p_addr = tc::smem_u32(p_buf);
-      int iq = 0, ip = 0, seg = -1, pseg = -1;
-      Cursor cq, cpv;
-      cq.init(u0, S);
-      cpv = cq;
-      IdleClock clk;
-      while (ip < T) {
-        bool progressed = false;
-        if (iq < T) {
-          const bool first = (iq == 0 || cq.t == 0);
-          const bool last = (iq == T - 1 || cq.t == cq.tb - 1);
-          const int qseg = first ? seg + 1 : seg;
-          const int qb = qseg % C::kQBufs;
-          const int ks = iq % NK, sb = iq & 1;
-          if (tc::mbar_test(&k_full[ks], (uint32_t)(iq / NK) & 1u) &&
-              tc::mbar_test(&s_empty[sb], ((uint32_t)(iq >> 1) & 1u) ^ 1u) &&
-              (!first || tc::mbar_test(&q_full[qb], (uint32_t)(qseg / C::kQBufs) & 1u))) {
-            seg = qseg;
-            tc::tc_fence_after();
-            const uint32_t k_addr = tc::smem_u32(k_ring + ks * C::kTileBytes);
-            const uint32_t q_addr = tc::smem_u32(q_buf) + qb * C::kQParts * C::kQPart;
-            const uint32_t d = tmem + sb * C::kNQP;
-            if constexpr (FP8) {
-              constexpr uint32_t idesc = tc::idesc_f8(kKT, NQ, false);
+    // ready.  The whole warp runs this, converged, and lane 0 alone issues: descriptors
+    // then stay in uniform registers, where the instruction wants them.  (Issued from a
+    // lane's own branch an MMA cost 77 cycles, more than the tensor cores take for it.)
+    constexpr uint32_t swz_code = C::kBoxRow == 128 ? 2u : 4u;
+    constexpr uint32_t p_swz = C::kPRow == 128 ? 2u : (C::kPRow == 64 ? 4u : 6u);
+    constexpr uint32_t full = 0xffffffffu;
+    const bool leader = lane == 0;
+    const uint32_t k_base = tc::smem_u32(k_ring), v_base = tc::smem_u32(v_ring);
+    const uint32_t q_base = tc::smem_u32(q_buf), p_base = tc::smem_u32(p_buf);
+    const uint32_t t_s = __shfl_sync(full, tmem, 0), t_o = t_s + 2 * C::kSCols;
+    int iq = 0, ip = 0, seg = -1, pseg = -1;
+    int ks = 0, vs = 0;           // stages of QK(iq) and PV(ip),
+    uint32_t kph = 0, vph = 0;    // and their phases
+    int seg_i0 = 0;               // range index of segment pseg's first tile
+    Cursor cq, cpv;
+    cq.init(u0, S);
+    cpv = cq;
+    // tiles left of the item that QK, PV is in
+    int q_left = __shfl_sync(full, min(cq.tb - cq.t, T), 0), pv_left = q_left;
+    bool q_opens = true, pv_opens = true;
+    IdleClock clk;
+    while (ip < T) {
+      bool progressed = false;
+      if (iq < T) {
+        const int qseg = q_opens ? seg + 1 : seg;
+        const int qb = C::kQBufs == 2 ? qseg & 1 : 0;
+        const int sb = iq & 1;
+        const bool ready = tc::mbar_test(&k_full[ks], kph) &&
+                           tc::mbar_test(&s_empty[sb], ((uint32_t)(iq >> 1) & 1u) ^ 1u) &&
+                           (!q_opens || tc::mbar_test(&q_full[qb], (uint32_t)(qseg / C::kQBufs) & 1u));
+        if (__all_sync(full, ready)) {
+          seg = qseg;
+          tc::tc_fence_after();
+          const uint32_t k_addr = k_base + ks * C::kTileBytes;
+          const uint32_t q_addr = q_base + qb * (C::kQParts * C::kQPart);
+          const uint32_t d = t_s + sb * C::kSCols;
+          if constexpr (FP8) {
+            constexpr uint32_t idesc = tc::idesc_f8(kKT, C::kSCols, false);
+            const uint64_t dk = tc::smem_desc(k_addr, 16, 8 * DH, swz_code);
+            const uint64_t dq = tc::smem_desc(q_addr, 16, 8 * DH, swz_code);
 #pragma unroll
-              for (int part = 0; part < 2; ++part)
+            for (int kk = 0; kk < DH / 32; ++kk)
+              if (leader) tc::mma_f8(d, dk + kk * 2, dq + kk * 2, idesc, kk != 0);
+          } else {
+            constexpr uint32_t idesc = tc::idesc_bf16(kKT, NQ, false, false);
+            const uint64_t dk = tc::smem_desc(k_addr, 16, 1024, 2);
+            const uint64_t dq = tc::smem_desc(q_addr, 16, 1024, 2);
 #pragma unroll
-                for (int kk = 0; kk < DH / 32; ++kk)
-                  tc::mma_f8(d, tc::smem_desc(k_addr + kk * 32, 16, 8 * DH, swz_code),
-                             tc::smem_desc(q_addr + part * C::kQPart + kk * 32, 16, 8 * DH, swz_code),
-                             idesc, part + kk != 0);
-            } else {
-              constexpr uint32_t idesc = tc::idesc_bf16(kKT, NQ, false, false);
-#pragma unroll
-              for (int kk = 0; kk < DH / 16; ++kk) {
-                const uint32_t ko = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
-                const uint32_t qo = (kk >> 2) * NQ * 128 + (kk & 3) * 32;
-                tc::mma_bf16(d, tc::smem_desc(k_addr + ko, 16, 1024, 2),
-                             tc::smem_desc(q_addr + qo, 16, 1024, 2), idesc, kk != 0);
-              }
-            }
+            for (int kk = 0; kk < DH / 16; ++kk)
+              if (leader)
+                tc::mma_bf16(d, dk + ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) / 16,
+                             dq + ((kk >> 2) * NQ * 128 + (kk & 3) * 32) / 16, idesc, kk != 0);
+          }
+          const bool closes = --q_left == 0;
+          if (leader) {
             tc::mma_commit(&s_full[sb]);
             tc::mma_commit(&k_empty[ks]);
-            if (last) tc::mma_commit(&q_empty[qb]);
-            if (++iq < T) cq.next(S);
-            progressed = true;
+            if (closes) tc::mma_commit(&q_empty[qb]);
           }
+          if (++ks == NK) {
+            ks = 0;
+            kph ^= 1u;
+          }
+          ++iq;
+          q_opens = closes;
+          if (closes && iq < T) {
+            cq.next_item(S);
+            q_left = __shfl_sync(full, min(cq.tb, T - iq), 0);
+          }
+          progressed = true;
         }
-        if (ip < iq) {
-          const int vs = ip % NV;
-          if (tc::mbar_test(&p_full[ip & 1], (uint32_t)(ip >> 1) & 1u) &&
-              tc::mbar_test(&v_full[vs], (uint32_t)(ip / NV) & 1u)) {
-            const bool first = (ip == 0 || cpv.t == 0);
-            if (first) ++pseg;
-            tc::tc_fence_after();
-            const uint32_t v_addr = tc::smem_u32(v_ring + vs * C::kTileBytes);
-            const uint32_t pb_addr = p_addr + (ip & 1) * C::kPBuf;
-            const uint32_t o_addr = tmem_o + (uint32_t)((pseg & 1) * C::kNQP);
-            if constexpr (FP8) {
-              constexpr uint32_t idesc = tc::idesc_f8(kKT, NQ, true, true, true);
+      }
+      if (ip < iq) {
+        const bool ready =
+            tc::mbar_test(&p_full[ip & 1], (uint32_t)(ip >> 1) & 1u) &&
+            tc::mbar_test(&v_full[vs], vph) &&
+            (!pv_opens || tc::mbar_test(&o_empty[(pseg + 1) & 1], ((uint32_t)((pseg + 1) >> 1) & 1u) ^ 1u));
+        if (__all_sync(full, ready)) {
+          if (pv_opens) {
+            ++pseg;
+            seg_i0 = ip;
+          }
+          const uint32_t set = ip - seg_i0 < C::kGroups;  // the group's first tile: O is set
+          tc::tc_fence_after();
+          const uint32_t v_addr = v_base + vs * C::kTileBytes;
+          const uint32_t pb_addr = p_base + (ip & 1) * C::kPBuf;
+          const uint32_t o_addr =
+              t_o + (uint32_t)(((pseg & 1) * C::kGroups + (C::kGroups == 2 ? ip & 1 : 0)) * C::kOCols);
+          if constexpr (FP8) {
+            constexpr uint32_t idesc = tc::idesc_f8(kKT, C::kOCols, true, true, true);
+            const uint64_t dv = tc::smem_desc(v_addr, 0, 8 * DH, swz_code);
+            const uint64_t dp = tc::smem_desc(pb_addr, 0, 8 * C::kPRow, p_swz);
 #pragma unroll
-              for (int part = 0; part < 3; ++part)
+            for (int kk = 0; kk < kKT / 32; ++kk)
+              if (leader)
+                tc::mma_f8(o_addr, dv + kk * 2 * DH, dp + kk * 2 * C::kPRow, idesc,
+                           kk == 0 ? set ^ 1u : 1u);
+          } else {
+            constexpr uint32_t idesc = tc::idesc_bf16(kKT, NQ, true, true);
+            const uint64_t dv = tc::smem_desc(v_addr, DH == 128 ? 16384 : 0, 1024, 2);
+            const uint64_t dp = tc::smem_desc(pb_addr, 0, 8 * C::kPRow, p_swz);
 #pragma unroll
-                for (int kk = 0; kk < kKT / 32; ++kk)
-                  tc::mma_f8(o_addr, tc::smem_desc(v_addr + kk * 32 * DH, 0, 8 * DH, swz_code),
-                             tc::smem_desc(pb_addr + part * C::kPPart + kk * 32 * C::kPRow, 0,
-                                           8 * C::kPRow, p_swz),
-                             idesc, (first && part + kk == 0) ? 0u : 1u);
-            } else {
-              constexpr uint32_t idesc = tc::idesc_bf16(kKT, NQ, true, true);
-#pragma unroll
-              for (int kk = 0; kk < kKT / 16; ++kk) {
-                const uint64_t da = tc::smem_desc(v_addr + kk * 2048, DH == 128 ? 16384 : 0, 1024, 2);
-                const uint64_t db = tc::smem_desc(pb_addr + kk * 16 * C::kPRow, 0, 8 * C::kPRow, p_swz);
-                tc::mma_bf16(o_addr, da, db, idesc, (first && kk == 0) ? 0u : 1u);
-              }
-            }
+            for (int kk = 0; kk < kKT / 16; ++kk)
+              if (leader)
+                tc::mma_bf16(o_addr, dv + kk * 128, dp + kk * C::kPRow, idesc,
+                             kk == 0 ? set ^ 1u : 1u);
+          }
+          const bool closes = --pv_left == 0;
+          if (leader) {
             tc::mma_commit(&pv_done[ip & 1]);
             tc::mma_commit(&v_empty[vs]);
-            if (++ip < T) cpv.next(S);
-            progressed = true;
           }
+          if (++vs == NV) {
+            vs = 0;
+            vph ^= 1u;
+          }
+          ++ip;
+          pv_opens = closes;
+          if (closes && ip < T) {
+            cpv.next_item(S);
+            pv_left = __shfl_sync(full, min(cpv.tb, T - ip), 0);
+          }
+          progressed = true;
         }
-        if (!progressed && !clk.idle(abort_flag, p.status)) break;
-        if (progressed) clk.reset();
       }
+      if (!progressed && __any_sync(full, !clk.idle(abort_flag, p.status))) break;
+      if (progressed) clk.reset();
     }
-  } else if (warp < C::kFinisher) {
+  } else if (warp >= C::kFirst) {
     // ------------------------------------------------------------ softmax / epilogue
-    // The warps that share a TMEM lane quarter split the rows: a thread owns one
-    // slot (later one dh row) and the NQH columns [c0, c0 + NQH).
-    constexpr int NQH = C::kCols;
-    const int st = tid - 64;                 // 0..kSmx-1
+    // Group `grp` takes the tiles with its parity (all of them when there is one
+    // group).  Its warps that share a TMEM lane quarter split the rows: a thread owns
+    // one slot and the columns [c0, c0 + 16); when results are written, one dh row and
+    // the columns [f0, f0 + NF).
+    constexpr int NQH = C::kCols, NF = C::kFinCols, GT = C::kGroupThreads, KG = C::kGroups;
+    const int st = tid - 32 * C::kFirst;     // 0..kSmx-1
+    const int grp = KG == 2 ? st / GT : 0;
+    const int gt = st - grp * GT;
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;        // column group
-    const int c0 = half * NQH;
+    const int c0 = (gt >> 7) * NQH;
+    const int f0 = (st >> 7) * NF;
     const int kl = quarter * 32 + lane;      // TMEM lane: slot of S^T, dh row of O^T
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    float l[NQH], mrun[NQH];
-#pragma unroll
-    for (int c = 0; c < NQH; ++c) {
-      l[c] = 0.f;
-      mrun[c] = kNone;
-    }
+    const int bar_a = 1 + 2 * grp, bar_b = 2 + 2 * grp;  // named barriers of the group
+    constexpr int kBarCount = 5, kBarAll = 6;
+    float* m_run = s_mrun + grp * 192;  // [64], then the rescales of l and of O
+    float* alpha = m_run + 64;
+    float* alpha_o = alpha + 64;
+    float* wred = s_wred + grp * 256;  // [4][64]
+    uint32_t* anc = s_anc + grp * 64 * kAncWords;
+    int* par = s_par + grp * kMaxNodes;
+    float l[NQH];
     int e_ref = -1000;     // power of two that the segment's weights are taken against
-    int seg = -1;
     int anc_key = -1;      // (chunk, sequence) whose ancestors are in shared memory
     int pv_waited = -1;    // index of the last PV this thread waited for
-    int seg_t0 = 0;        // tile at which the segment started
-    int n_done = 0;        // segments whose last tile is through
-    int n_fin = 0;         // segments whose result is written
-    int end0 = 0, end1 = 0;  // last tile (range index) of the segment in O buffer 0 / 1
     Cursor cs;
     cs.init(u0, S);
     const int item0 = u0 - cs.t;  // first unit of the item the range starts in
 
     // Where the item's rows go in out, and how many columns are rows of the sequence.
     auto out_of = [&](int qc, int b, int h) {
-      return p.out + (((size_t)b * p.T + qc * p.tn) * p.Hq + h * p.g) * DH + kl;
+      return p.out +
+             (((size_t)b * p.T + qc / p.hs * p.tn) * p.Hq + h * p.g + qc % p.hs * p.gs) * DH + kl;
     };
-    auto columns = [&](int qc, int b) { return min(p.tn, s_nn[b] - qc * p.tn) * p.g; };
+    auto columns = [&](int qc, int b) {  // (with hs = 2 a chunk has one node)
+      return min(p.tn, s_nn[b] - qc / p.hs * p.tn) * min(p.gs, p.g - qc % p.hs * p.gs);
+    };
+    auto wait_pv = [&](int e) {
+      if (e >= 0 && pv_waited < e) {
+        // after a timeout every later wait returns at once: keep going, so that all
+        // threads still meet at the same barriers
+        tc::mbar_wait(&pv_done[e & 1], (uint32_t)(e >> 1) & 1u, abort_flag, p.status);
+        pv_waited = e;
+      }
+    };
 
-    // Writes segment s's result from its O buffer, once its last PV is done: the
-    // output of a whole item, or this CTA's partial of a split one, whose arrival on
-    // fin_full hands it to the finisher.
-    auto finish = [&](int s) {
-      const int sl = s & 1;
-      const int qc = I->seg_at[sl] & 0x3fffffff, b = I->seg_b[sl], h = I->seg_h[sl];
-      const float unit = FP8 ? exp2f((float)(I->seg_e[sl] - C::kPOff)) : 1.f;  // of O
-      const uint32_t t_o = tmem_o + (uint32_t)(sl * C::kNQP) + lane_off + (uint32_t)c0;
-      const float* sm = seg_m + sl * 64;
-      const float* sls = seg_l + sl * 64;
-      const bool bad = I->seg_bad[sl] != 0;
-      if (I->seg_at[sl] >> 30) {
-        __nv_bfloat16* o_at = out_of(qc, b, h);
-        const int ncol = columns(qc, b);
+    // The last segment this group closed, and what has become of it.
+    int d_seg = -1;
+    bool d_pub = true, d_fin = true;
+
+    // Tells the other group that this one's O of the closed segment is final.
+    auto publish = [&]() {
+      wait_pv(I->item[d_seg & 1][grp][5]);
+      tc::tc_fence_after();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&seg_full[d_seg & 1]);
+      d_pub = true;
+    };
+    // Writes the closed segment's result from both groups' O: the output of a whole
+    // item, or this CTA's partial of a split one, whose arrival on fin_full hands it to
+    // the finisher.
+    auto finish = [&]() {
+      const int sl = d_seg & 1;
+      const int* it = I->item[sl][grp];
+      const int d_qc = it[0], d_b = it[1], d_h = it[2];
+      tc::mbar_wait(&seg_full[sl], (uint32_t)(d_seg >> 1) & 1u, abort_flag, p.status);
+      tc::tc_fence_after();
+      const float* sm = seg_m + sl * 128;  // [group][64]
+      const float* ls = seg_l + sl * 128;
+      float o[NF];
+      bool bad = false;
 #pragma unroll
-        for (int cc = 0; cc < NQH; cc += 16) {
-          const int w = NQH - cc < 16 ? NQH - cc : 16;
-          float o[16];
-          tmem_ld_chunk(t_o + cc, o, w);
+      for (int x = 0; x < KG; ++x) {
+        // a group without a tile in the segment has left its O as it was
+        const bool has = I->seg_has[sl][x] != 0;
+        bad |= I->seg_bad[sl][x] != 0;
+        const float unit = FP8 ? exp2f((float)(I->seg_e[sl][x] - C::kPOff)) : 1.f;
+        float y[NF];
+        const uint32_t at = tmem_o + (uint32_t)((sl * KG + x) * C::kOCols) + lane_off + (uint32_t)f0;
+        tmem_ld_chunk(at, y, NF);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int part = 1; part < C::kOParts; ++part) {
+          float z[NF];
+          tmem_ld_chunk(at + part * NQ, z, NF);
           tc::tmem_wait_ld();
-          if (kl < DH) {
 #pragma unroll
-            for (int c = 0; c < w; ++c)
-              if (c0 + cc + c < ncol)
-                o_at[col_off[c0 + cc + c]] =
-                    __float2bfloat16_rn(__fdividef(o[c] * unit, sls[c0 + cc + c]));
-          }
+          for (int c = 0; c < NF; ++c) y[c] += z[c];
         }
-        if (bad && kl < DH) add_unfit<DH, FP8>(p, qc, b, h, s_len[b], s_nn[b], c0, c0 + NQH, kl);
+#pragma unroll
+        for (int c = 0; c < NF; ++c) {
+          float w = unit;
+          if (KG == 2) w *= exp2f(sm[x * 64 + f0 + c] - fmaxf(sm[f0 + c], sm[64 + f0 + c]));
+          const float v = has ? y[c] * w : 0.f;
+          o[c] = x == 0 ? v : o[c] + v;
+        }
+      }
+      auto sums = [&](int c) {  // l of column c, both groups at the larger maximum
+        if (KG == 1) return ls[c];
+        const float M = fmaxf(sm[c], sm[64 + c]);
+        return exp2f(sm[c] - M) * ls[c] + exp2f(sm[64 + c] - M) * ls[64 + c];
+      };
+      if (it[4]) {
+        __nv_bfloat16* o_at = out_of(d_qc, d_b, d_h);
+        const int ncol = columns(d_qc, d_b);
+        if (kl < DH) {
+#pragma unroll
+          for (int c = 0; c < NF; ++c)
+            if (f0 + c < ncol)
+              o_at[col_off[f0 + c]] = __float2bfloat16_rn(__fdividef(o[c], sums(f0 + c)));
+          if (bad) add_unfit<DH, FP8>(p, d_qc, d_b, d_h, s_len[d_b], s_nn[d_b], f0, f0 + NF, kl);
+        }
       } else {
         // slot 0 for the item the range starts in, 1 for the one it ends in
-        const int slot = (I->seg_u[sl] == item0) ? 0 : 1;
+        const int slot = (it[3] == item0) ? 0 : 1;
         float* part = p.partials + ((size_t)cta * 2 + slot) * C::kPartFloats;
+        if (kl < DH) {
+          // O as [NQ / 4][dh row][4]: a warp's 16-byte accesses are consecutive
+          float4* dst = reinterpret_cast<float4*>(part) + f0 / 4 * DH + kl;
 #pragma unroll
-        for (int cc = 0; cc < NQH; cc += 16) {
-          const int w = NQH - cc < 16 ? NQH - cc : 16;
-          float o[16];
-          tmem_ld_chunk(t_o + cc, o, w);
-          tc::tmem_wait_ld();
-          if (kl < DH) {
-            // O as [NQ / 4][dh row][4]: a warp's 16-byte accesses are consecutive
-            float4* dst = reinterpret_cast<float4*>(part) + (c0 + cc) / 4 * DH + kl;
-#pragma unroll
-            for (int v = 0; v < w / 4; ++v)
-              dst[v * DH] = make_float4(o[4 * v] * unit, o[4 * v + 1] * unit, o[4 * v + 2] * unit,
-                                   o[4 * v + 3] * unit);
-          }
+          for (int v = 0; v < NF / 4; ++v)
+            dst[v * DH] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
         }
         if (st < NQ) {
-          part[(size_t)NQ * DH + st] = sm[st];
-          part[(size_t)NQ * DH + NQ + st] = sls[st];
+          part[(size_t)NQ * DH + st] = KG == 1 ? sm[st] : fmaxf(sm[st], sm[64 + st]);
+          part[(size_t)NQ * DH + NQ + st] = sums(st);
         }
         if (st == 0) part[(size_t)NQ * DH + 2 * NQ] = bad ? 1.f : 0.f;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&fin_full[slot]);
       }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&o_empty[sl]);
+      d_fin = true;
     };
 
-    // 8 bits: the tile's slot scales, one tile ahead
-    float nks = 0.f, nvs = 0.f;
+    // 8 bits: the tile's slot scales, one tile ahead, by the thread that reads them.
+    // (Through shared memory: in registers they were spilled, which waits for the load.)
+    float2* scales = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(s_pre) + Misc::seq_bytes(p.B)) + st;
     size_t sc_head = 0;  // the head's first scale
     auto load_scales = [&](int t) {
       const size_t i = sc_head + min(t * kKT + kl, p.N - 1);
-      nks = ld_early(p.k_scale + i);
-      nvs = ld_early(p.v_scale + i);
+      copy_async4(&scales->x, p.k_scale + i);
+      copy_async4(&scales->y, p.v_scale + i);
     };
-    auto head_of = [&](const Cursor& at) { return ((size_t)at.b * p.Hkv + at.h) * p.N; };
+
+    int i0 = 0;  // range index of the segment's first tile
     if constexpr (FP8) {
-      sc_head = head_of(cs);
-      load_scales(cs.t);
+      sc_head = ((size_t)cs.b * p.Hkv + cs.h) * p.N;
+      load_scales(cs.t + (KG == 2 ? grp : 0));
       // the range's first Q is split by all of these warps: nothing else is to do yet
-      split_q<NQ, DH>(p, cs.qc, cs.b, cs.h, s_nn[cs.b], warp - 2, kSmx / 32, q_buf, qsc);
+      int* w_max = reinterpret_cast<int*>(qsc) + 2;
+      const float unit = split_q<NQ, DH, C::kSmx / 32>(
+          p, cs.qc, cs.b, cs.h, s_nn[cs.b], warp - C::kFirst, q_buf, [&](uint32_t mx) {
+            if (lane == 0) w_max[warp - C::kFirst] = (int)mx;
+            tc::named_bar_sync(kBarAll, C::kSmx);
+            return __reduce_max_sync(0xffffffffu, (uint32_t)w_max[lane & (C::kSmx / 32 - 1)]);
+          });
+      if (st == 0) qsc[0] = unit;
       tc::fence_proxy_async_smem();
-      tc::named_bar_sync(1, kSmx);
-      if (st == 0) tc::mbar_arrive(&q_full[0]);
+      tc::named_bar_sync(kBarAll, C::kSmx);
+      if (st < 64 && lane == 0) tc::mbar_arrive(&q_full[0]);  // twice
     }
 
-    int len = s_len[cs.b], lim = len + s_nn[cs.b];
-    for (int i = 0; i < T; ++i) {
-      const int t = cs.t, qc = cs.qc, b = cs.b;
-      const bool first = (i == 0 || t == 0);
-      const bool last = (i == T - 1 || t == cs.tb - 1);
-      const bool tree = (t + 1) * kKT > len;  // the tile holds nodes (or slots past them)
-      const int iu = u0 + i - t;              // the item's first unit
-      if (first) {
-        ++seg;
-        seg_t0 = t;
-        e_ref = -1000;
-      }
-      if (tree && b * p.n_qc + qc != anc_key) {
-        // the chunk's nodes' ancestors, a thread a node
-        anc_key = b * p.n_qc + qc;
-        tc::named_bar_sync(1, kSmx);  // nobody reads the old ones any more
-        if (p.parent)
-          for (int n = st; n < s_nn[b]; n += kSmx) s_par[n] = p.parent[(size_t)b * p.T + n];
-        for (int w = st; w < p.tn * kAncWords; w += kSmx) anc[w] = 0u;
-        tc::named_bar_sync(1, kSmx);
-        int n = qc * p.tn + st;
-        if (st < p.tn && n < s_nn[b]) {
-          uint32_t* a = anc + st * kAncWords;
-          if (p.parent) {
+    for (int seg = 0;; ++seg) {
+      // ---- a segment: the tiles [i0, i0 + nt) of one item; behind the last an empty one
+      const int nt = min(cs.tb - cs.t, T - i0);
+      const int qc = cs.qc, b = cs.b;
+      const int len = s_len[b], lim = len + s_nn[b];
+      bool first = true;
+      int last = -1;
+      e_ref = -1000;
+#pragma unroll
+      for (int c = 0; c < NQH; ++c) l[c] = 0.f;
 #pragma unroll 1
-            while (n >= 0) {
-              a[n >> 5] |= 1u << (n & 31);
-              int up = s_par[n];
-              if (up < -1 || up >= n) {
-                set_status(p.status, FDLLM_ERR_BAD_INDEX);
-                up = -1;
+      for (int i = KG == 2 ? i0 + ((i0 ^ grp) & 1) : i0;; i += KG) {
+        const bool closing = i + KG >= i0 + nt;
+        if (i < i0 + nt) {
+        const int t = cs.t + i - i0;
+        const bool tree = (t + 1) * kKT > len;  // the tile holds nodes (or slots past them)
+        if (tree && b * p.n_qc + qc != anc_key) {
+          // the chunk's nodes' ancestors, a thread a node
+          anc_key = b * p.n_qc + qc;
+          tc::named_bar_sync(bar_a, GT);  // nobody reads the old ones any more
+          if (p.parent)
+            for (int n = gt; n < s_nn[b]; n += GT) par[n] = p.parent[(size_t)b * p.T + n];
+          for (int w = gt; w < p.tn * kAncWords; w += GT) anc[w] = 0u;
+          tc::named_bar_sync(bar_a, GT);
+          int n = qc / p.hs * p.tn + gt;
+          if (gt < p.tn && n < s_nn[b]) {
+            uint32_t* a = anc + gt * kAncWords;
+            if (p.parent) {
+#pragma unroll 1
+              while (n >= 0) {
+                a[n >> 5] |= 1u << (n & 31);
+                int up = par[n];
+                if (up < -1 || up >= n) {
+                  set_status(p.status, FDLLM_ERR_BAD_INDEX);
+                  up = -1;
+                }
+                n = up;
               }
-              n = up;
+            } else {
+#pragma unroll 1
+              for (int w = 0; w <= n >> 5; ++w)
+                a[w] = w < (n >> 5) ? ~0u : ~0u >> (31 - (n & 31));
+            }
+          }
+          tc::named_bar_sync(bar_a, GT);
+        }
+        float ksc = p.qk_scale, vs = 1.f;
+        if constexpr (FP8) {
+          copy_async_wait();
+          const float2 f = *scales;
+          ksc *= f.x * qsc[seg & 1];
+          vs = f.y;
+          if (i + KG < i0 + nt) load_scales(t + KG);
+        }
+        const int slot = t * kKT + kl;
+        const bool zero_v = tree && slot >= lim;  // this slot's V goes into no sum
+
+        const int sb = i & 1;
+        tc::mbar_wait(&s_full[sb], (uint32_t)(i >> 1) & 1u, abort_flag, p.status);
+        tc::tc_fence_after();
+
+        // ---- scores (log2 units) against the running maximum: row kl of S^T, this
+        // thread's columns.  The maximum is raised when a score exceeds it by more than
+        // 2^kThresh (masked scores never do); a segment's first tile sets it.  Then the
+        // scores are formed again, as they are for their maxima (pass 1) and against the
+        // new maximum (pass 2): one copy of the code, S being there until the end.
+        float d[NQH];  // exponents of the weights
+        int pass = first ? 1 : 0;
+        bool any = first;
+#pragma unroll 1
+        for (;;) {
+          const uint32_t at = tmem + lane_off + sb * C::kSCols + c0;
+#pragma unroll
+          for (int c = 0; c < NQH; c += 16) tmem_ld_chunk(at + c, d + c, 16);
+          if constexpr (FP8) {
+            float d2[NQH];
+#pragma unroll
+            for (int c = 0; c < NQH; c += 16) tmem_ld_chunk(at + NQ + c, d2 + c, 16);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < NQH; ++c) d[c] += d2[c];
+          } else {
+            tc::tmem_wait_ld();
+          }
+          const float4* m4 = reinterpret_cast<const float4*>((pass == 1 ? s_zero : m_run) + c0);
+#pragma unroll
+          for (int c = 0; c < NQH; c += 4) {
+            const float4 m = m4[c / 4];
+            d[c] = fmaf(d[c], ksc, -m.x);
+            d[c + 1] = fmaf(d[c + 1], ksc, -m.y);
+            d[c + 2] = fmaf(d[c + 2], ksc, -m.z);
+            d[c + 3] = fmaf(d[c + 3], ksc, -m.w);
+          }
+          if (tree) {
+            const int j = slot - len;
+            if (slot >= lim) {
+#pragma unroll
+              for (int c = 0; c < NQH; ++c) d[c] = -INFINITY;
+            } else if (j >= 0) {
+              const uint32_t* aw = anc + (j >> 5);
+#pragma unroll
+              for (int c = 0; c < NQH; ++c)
+                if (!((aw[(int)col_node[c0 + c] * kAncWords] >> (j & 31)) & 1u)) d[c] = -INFINITY;
+            }
+          }
+          if (pass == 2) break;
+          int vexp = -1000;
+          if constexpr (FP8) {
+            // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1), at least
+            // 2^-100; scales of slots that go into no sum, zero ones and those that are
+            // not finite do not count
+            const int eb = (__float_as_int(vs) >> 23) & 255;
+            if (!zero_v && eb > 0 && eb < 255) vexp = max(eb - 127, -100);
+          }
+          if (pass == 0) {
+            float top = d[0];
+#pragma unroll
+            for (int c = 1; c < NQH; ++c) top = fmaxf(top, d[c]);
+            any = bar_any(bar_b, GT, top > C::kThresh || (FP8 && vexp > e_ref));
+            if (!any) break;
+            pass = 1;
+            continue;
+          }
+#pragma unroll
+          for (int c = 0; c < NQH; ++c) {
+            const float wm = warp_max(d[c]);
+            if (lane == c) wred[quarter * 64 + c0 + c] = wm;
+          }
+          if constexpr (FP8) {
+            const int e = __reduce_max_sync(0xffffffffu, vexp);
+            if (lane == 0 && c0 == 0) I->vexp[grp][quarter] = e;
+          }
+          tc::named_bar_sync(bar_a, GT);
+          float e_scale = 1.f;
+          if constexpr (FP8) {
+            int e_new = e_ref;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) e_new = max(e_new, I->vexp[grp][w]);
+            // 2^(e_ref - e_new): 0 from the start value
+            e_scale = e_ref - e_new < -126 ? 0.f : __int_as_float((e_ref - e_new + 127) << 23);
+            e_ref = e_new;
+          }
+          if (gt < NQ) {
+            const float mo = first ? kNone : m_run[gt];
+            const float tm = fmaxf(fmaxf(wred[gt], wred[64 + gt]), fmaxf(wred[128 + gt], wred[192 + gt]));
+            const float mn = (tm - mo > C::kThresh) ? tm : mo;
+            const float al = exp2f(mo - mn);
+            alpha[gt] = al;
+            alpha_o[gt] = al * e_scale;
+            m_run[gt] = mn;
+          }
+          tc::named_bar_sync(bar_a, GT);
+#pragma unroll
+          for (int c = 0; c < NQH; ++c) l[c] *= alpha[c0 + c];
+          pass = 2;
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s_empty[sb]);
+
+        // ---- P buffer i&1 is free once PV(i-2) is done; rescaling O needs the group's
+        // last PV
+        wait_pv(i - 2);
+        if (any && !first) {
+          if (KG == 1) wait_pv(i - 1);
+          tc::tc_fence_after();
+          const uint32_t at =
+              tmem_o + (uint32_t)(((seg & 1) * KG + grp) * C::kOCols) + lane_off + (uint32_t)c0;
+          float o[8];
+#pragma unroll 1
+          for (int cc = 0; cc < C::kOParts * NQH; cc += 8) {
+            const int c1 = cc & (NQH - 1), part = cc / NQH;
+            tc::tmem_ld8(at + part * NQ + c1, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] *= alpha_o[c0 + c1 + c];
+            tc::tmem_st8(at + part * NQ + c1, o);
+          }
+          tc::tmem_wait_st();
+        }
+        if (tree && slot >= len && c0 == 0) {
+          // V of a slot past the nodes: zeros; of a node: zeros in place of what is not
+          // finite
+          tc::mbar_wait(&v_full[i % NV], (uint32_t)(i / NV) & 1u, abort_flag, p.status);
+          uint8_t* row = v_ring + (i % NV) * C::kTileBytes + kl * C::kBoxRow;
+          if (zero_v) {
+#pragma unroll 2
+            for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
+              const int x = q / (C::kBoxRow / 16);
+              *reinterpret_cast<uint4*>(row + x * C::kBoxBytes + (q - x * (C::kBoxRow / 16)) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
             }
           } else {
-#pragma unroll 1
-            for (int w = 0; w <= n >> 5; ++w) a[w] = w < (n >> 5) ? ~0u : ~0u >> (31 - (n & 31));
-          }
-        }
-        tc::named_bar_sync(1, kSmx);
-      }
-      float ksc = p.qk_scale, vs = 1.f;
-      if constexpr (FP8) {
-        ksc *= nks;
-        vs = nvs;
-      }
-      if constexpr (FP8) {
-        if (!last) load_scales(t + 1);
-      }
-      const uint32_t t_oc = tmem_o + (uint32_t)((seg & 1) * C::kNQP);  // this segment's O
-
-      // ---- scores of this tile: row kl of S^T, this thread's columns
-      const int sb = i & 1;
-      // after a timeout every later wait returns at once: keep going, so that all
-      // softmax threads still meet at the same named barriers
-      tc::mbar_wait(&s_full[sb], (uint32_t)(i >> 1) & 1u, abort_flag, p.status);
-      tc::tc_fence_after();
-      float s[NQH];
-#pragma unroll
-      for (int c = 0; c < NQH; c += 16)
-        tmem_ld_chunk(tmem + lane_off + sb * C::kNQP + c0 + c, s + c, NQH - c < 16 ? NQH - c : 16);
-      tc::tmem_wait_ld();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&s_empty[sb]);
-
-      // s becomes the score in log2 units
-      if constexpr (FP8) {
-        const float4* qs4 = reinterpret_cast<const float4*>(qsc + (seg & 1) * 64 + c0);
-#pragma unroll
-        for (int c = 0; c < NQH; c += 4) {
-          const float4 f = qs4[c / 4];
-          s[c] *= ksc * f.x;
-          s[c + 1] *= ksc * f.y;
-          s[c + 2] *= ksc * f.z;
-          s[c + 3] *= ksc * f.w;
-        }
-        if (last) {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&q_empty[seg & 1]);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < NQH; ++c) s[c] *= ksc;
-      }
-      const int slot = t * kKT + kl;
-      bool zero_v = false;  // this slot's V goes into no sum
-      if (tree) {
-        const int j = slot - len;
-        if (slot >= lim) {
-          zero_v = true;
-#pragma unroll
-          for (int c = 0; c < NQH; ++c) s[c] = -INFINITY;
-        } else if (j >= 0) {
-          const uint32_t* aw = anc + (j >> 5);
-#pragma unroll
-          for (int c = 0; c < NQH; ++c)
-            if (!((aw[(int)col_node[c0 + c] * kAncWords] >> (j & 31)) & 1u)) s[c] = -INFINITY;
-        }
-      }
-
-      // ---- running maximum: raised when a score exceeds it by more than 2^kThresh
-      // (masked scores never do); a segment's first tile sets it
-      float d[NQH];  // exponents of the weights
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < NQH; ++c) {
-        d[c] = s[c] - mrun[c];
-        top = fmaxf(top, d[c]);
-      }
-      bool need = first || top > C::kThresh;
-      int vexp = -1000;
-      if constexpr (FP8) {
-        // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1), at least 2^-100;
-        // scales of slots that go into no sum, zero ones and those that are not finite
-        // do not count
-        const int eb = (__float_as_int(vs) >> 23) & 255;
-        if (!zero_v && eb > 0 && eb < 255) vexp = max(eb - 127, -100);
-        need |= vexp > e_ref;
-      }
-      const bool any = bar_any(2, kSmx, need);
-      if (any) {
-        if (first && st == 0) I->seg_bad[seg & 1] = 0;  // every thread is past finish(seg - 2)
-#pragma unroll
-        for (int c = 0; c < NQH; ++c) {
-          const float wm = warp_max(s[c]);
-          if (lane == (c & 31)) wred[quarter * 64 + c0 + c] = wm;
-        }
-        if constexpr (FP8) {
-          const int e = __reduce_max_sync(0xffffffffu, vexp);
-          if (lane == 0 && half == 0) I->vexp[quarter] = e;
-        }
-        tc::named_bar_sync(1, kSmx);
-        int e_new = e_ref;
-        float e_scale = 1.f;
-        if constexpr (FP8) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) e_new = max(e_new, I->vexp[w]);
-          // 2^(e_ref - e_new): 0 from the start value
-          e_scale = e_ref - e_new < -126 ? 0.f : __int_as_float((e_ref - e_new + 127) << 23);
-          e_ref = e_new;
-        }
-        if (st < NQ) {
-          const float mo = first ? kNone : m_run[st];
-          const float tm = fmaxf(fmaxf(wred[st], wred[64 + st]), fmaxf(wred[128 + st], wred[192 + st]));
-          const float mn = (tm - mo > C::kThresh) ? tm : mo;
-          const float al = exp2f(mo - mn);
-          alpha[st] = al;
-          alpha_o[st] = al * e_scale;
-          m_run[st] = mn;
-        }
-        tc::named_bar_sync(1, kSmx);
-#pragma unroll
-        for (int c = 0; c < NQH; ++c) {
-          mrun[c] = m_run[c0 + c];
-          d[c] = s[c] - mrun[c];
-          l[c] *= alpha[c0 + c];
-        }
-      }
-
-      // ---- P buffer i&1 is free once PV(i-2) is done; rescaling O needs PV(i-1)
-      if (i >= 2 && pv_waited < i - 2) {
-        tc::mbar_wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1) & 1u, abort_flag, p.status);
-        pv_waited = i - 2;
-      }
-      if (any && !first && pv_waited < i - 1) {
-        tc::mbar_wait(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, abort_flag, p.status);
-        pv_waited = i - 1;
-      }
-      tc::tc_fence_after();
-      if (any && !first) {
-        float o[16];
-#pragma unroll
-        for (int cc = 0; cc < NQH; cc += 16) {
-          const int w = NQH - cc < 16 ? NQH - cc : 16;
-          tmem_ld_chunk(t_oc + lane_off + c0 + cc, o, w);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < w; ++c) o[c] *= alpha_o[c0 + cc + c];
-          tmem_st_chunk(t_oc + lane_off + c0 + cc, o, w);
-        }
-        tc::tmem_wait_st();
-      }
-      if (tree && slot >= len && half == 0) {
-        // V of a slot past the nodes: zeros; of a node: zeros in place of what is not finite
-        tc::mbar_wait(&v_full[i % NV], (uint32_t)(i / NV) & 1u, abort_flag, p.status);
-        uint8_t* row = v_ring + (i % NV) * C::kTileBytes + kl * C::kBoxRow;
-        if (zero_v) {
-#pragma unroll 2
-          for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
-            const int x = q / (C::kBoxRow / 16);
-            *reinterpret_cast<uint4*>(row + x * C::kBoxBytes + (q - x * (C::kBoxRow / 16)) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-        } else {
-          // an exponent of all ones (an e4m3 of all ones) carries into the sign's place
-          constexpr uint32_t ones = FP8 ? 0x7f7f7f7fu : 0x7f807f80u;
-          constexpr uint32_t one = FP8 ? 0x01010101u : 0x00800080u;
-          constexpr uint32_t sign = FP8 ? 0x80808080u : 0x80008000u;
-          uint32_t hit = 0u;
+            // an exponent of all ones (an e4m3 of all ones) carries into the sign's place
+            constexpr uint32_t ones = FP8 ? 0x7f7f7f7fu : 0x7f807f80u;
+            constexpr uint32_t one = FP8 ? 0x01010101u : 0x00800080u;
+            constexpr uint32_t sign = FP8 ? 0x80808080u : 0x80008000u;
+            uint32_t hit = 0u;
 #pragma unroll 4
-          for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
-            const int x = q / (C::kBoxRow / 16);
-            const uint4 w = *reinterpret_cast<const uint4*>(row + x * C::kBoxBytes +
-                                                            (q - x * (C::kBoxRow / 16)) * 16);
-            hit |= ((w.x & ones) + one) | ((w.y & ones) + one) | ((w.z & ones) + one) |
-                   ((w.w & ones) + one);
+            for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
+              const int x = q / (C::kBoxRow / 16);
+              const uint4 w = *reinterpret_cast<const uint4*>(row + x * C::kBoxBytes +
+                                                              (q - x * (C::kBoxRow / 16)) * 16);
+              hit |= ((w.x & ones) + one) | ((w.y & ones) + one) | ((w.z & ones) + one) |
+                     ((w.w & ones) + one);
+            }
+            if ((hit & sign) != 0u) zero_unfit<FP8>(row, C::kBoxRow, C::kBoxes, C::kBoxBytes);
+            if ((hit & sign) != 0u || (FP8 && not_finite(vs))) I->bad_run[grp] = 1;
           }
-          if ((hit & sign) != 0u) zero_unfit<FP8>(row, C::kBoxRow, C::kBoxes, C::kBoxBytes);
-          if ((hit & sign) != 0u || (FP8 && not_finite(vs))) I->seg_bad[seg & 1] = 1;
         }
-      }
 
-      // ---- P = 2^(s - m) into row kl of the MN-major swizzled P^T tile
-      uint8_t* pb = p_buf + (i & 1) * C::kPBuf;
-      if constexpr (FP8) {
-        // the weight carries the slot's scale against 2^e_ref, times 2^kPOff
-        float w = 0.f;
-        if (!zero_v && !(tree && slot >= len && not_finite(vs)))
-          w = vs * __int_as_float((127 + min(C::kPOff - e_ref, 127)) << 23);
-        uint32_t pk[3][NQH / 4];
+        // ---- P = 2^(s - m) into row kl of the MN-major swizzled P^T tile
+        uint8_t* pb = p_buf + (i & 1) * C::kPBuf;
+        if constexpr (FP8) {
+          // the weight carries the slot's scale against 2^e_ref, times 2^kPOff
+          float w = 0.f;
+          if (!zero_v && !(tree && slot >= len && not_finite(vs)))
+            w = vs * __int_as_float((127 + min(C::kPOff - e_ref, 127)) << 23);
+          uint32_t pk[3][NQH / 4];
 #pragma unroll
-        for (int c = 0; c < NQH; c += 4) {
-          uint32_t hp[2][3];
+          for (int c = 0; c < NQH; c += 4) {
+            uint32_t hp[2][3];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float p0 = ex2_approx(d[c + 2 * y]);
-            const float p1 = ex2_approx(d[c + 2 * y + 1]);
-            l[c + 2 * y] += p0;
-            l[c + 2 * y + 1] += p1;
-            // fp16 value h; its upper byte is e5m2, cut off: h = hi + rest, twice; the
-            // last part is rounded (half a unit added below the byte; it never carries
-            // past 16 bits, parts being far below the largest)
-            const uint32_t h = pack_f16x2(p0 * w, p1 * w);
-            const uint32_t h1 = h & 0xff00ff00u;
-            const uint32_t r1 = sub_f16x2(h, h1);
-            const uint32_t h2 = r1 & 0xff00ff00u;
-            const uint32_t r2 = sub_f16x2(r1, h2);
-            hp[y][0] = h1;
-            hp[y][1] = h2;
-            hp[y][2] = r2 + 0x00800080u;
+            for (int y = 0; y < 2; ++y) {
+              const float p0 = ex2_approx(d[c + 2 * y]);
+              const float p1 = ex2_approx(d[c + 2 * y + 1]);
+              l[c + 2 * y] += p0;
+              l[c + 2 * y + 1] += p1;
+              // fp16 value h; its upper byte is e5m2, cut off: h = hi + rest, twice; the
+              // last part is rounded (half a unit added below the byte; it never carries
+              // past 16 bits, parts being far below the largest)
+              const uint32_t h = pack_f16x2(p0 * w, p1 * w);
+              const uint32_t h1 = h & 0xff00ff00u;
+              const uint32_t r1 = sub_f16x2(h, h1);
+              const uint32_t h2 = r1 & 0xff00ff00u;
+              const uint32_t r2 = sub_f16x2(r1, h2);
+              hp[y][0] = h1;
+              hp[y][1] = h2;
+              hp[y][2] = r2 + 0x00800080u;
+            }
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+              pk[part][c / 4] = __byte_perm(hp[0][part], hp[1][part], 0x7531);
           }
-          pk[0][c / 4] = __byte_perm(hp[0][0], hp[1][0], 0x7531);
-          pk[1][c / 4] = __byte_perm(hp[0][1], hp[1][1], 0x7531);
-          pk[2][c / 4] = __byte_perm(hp[0][2], hp[1][2], 0x7531);
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int ch = 0; ch < NQH / 16; ++ch)
+              *reinterpret_cast<uint4*>(
+                  pb + swz((uint32_t)(kl * C::kPRow + part * NQ + c0 + ch * 16), C::kPRow)) =
+                  make_uint4(pk[part][4 * ch], pk[part][4 * ch + 1], pk[part][4 * ch + 2],
+                             pk[part][4 * ch + 3]);
+        } else {
+          uint32_t pk[NQH / 2];
+#pragma unroll
+          for (int c = 0; c < NQH; c += 2) {
+            const float p0 = ex2_approx(d[c]);
+            const float p1 = ex2_approx(d[c + 1]);
+            l[c] += p0;
+            l[c + 1] += p1;
+            pk[c / 2] = pack_bf16x2(p0, p1);
+          }
+#pragma unroll
+          for (int ch = 0; ch < NQH / 8; ++ch)
+            *reinterpret_cast<uint4*>(pb + swz((uint32_t)(kl * C::kPRow + c0 * 2 + ch * 16), C::kPRow)) =
+                make_uint4(pk[ch * 4], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
         }
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int ch = 0; ch < NQH / 16; ++ch)
-            *reinterpret_cast<uint4*>(pb + part * C::kPPart +
-                                      swz((uint32_t)(kl * C::kPRow + c0 + ch * 16), C::kPRow)) =
-                make_uint4(pk[part][ch * 4], pk[part][ch * 4 + 1], pk[part][ch * 4 + 2],
-                           pk[part][ch * 4 + 3]);
-      } else {
-        uint32_t pk[NQH / 2];
-#pragma unroll
-        for (int c = 0; c < NQH; c += 2) {
-          const float p0 = ex2_approx(d[c]);
-          const float p1 = ex2_approx(d[c + 1]);
-          l[c] += p0;
-          l[c + 1] += p1;
-          pk[c / 2] = pack_bf16x2(p0, p1);
-        }
-#pragma unroll
-        for (int ch = 0; ch < NQH / 8; ++ch)
-          *reinterpret_cast<uint4*>(pb + swz((uint32_t)(kl * C::kPRow + c0 * 2 + ch * 16), C::kPRow)) =
-              make_uint4(pk[ch * 4], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
-      }
-      tc::fence_proxy_async_smem();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&p_full[i & 1]);
+        tc::fence_proxy_async_smem();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[i & 1]);
+        first = false;
+        last = i;
 
-      if (last) {
-        // ---- segment done: l summed per column; (m, l) are kept for its finish
+        }
+
+        // ---- the segment before: final once its last PV is two tiles back, written a
+        // tile later, off this one's path; at the latest when this one is closed, whose
+        // successor reuses its O
+        do {
+          if (!d_pub)
+            publish();
+          else if (!d_fin)
+            finish();
+        } while (closing && !d_fin);
+        if (closing) break;
+      }
+      if (i0 == T) break;
+
+      // ---- close the segment
+      if (last >= 0) {
 #pragma unroll
         for (int c = 0; c < NQH; ++c) {
           float v = l[c];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == (c & 31)) wred[quarter * 64 + c0 + c] = v;
-          l[c] = 0.f;
-          mrun[c] = kNone;
+          if (lane == c) wred[quarter * 64 + c0 + c] = v;
         }
-        tc::named_bar_sync(1, kSmx);
-        const int sl = seg & 1;
-        if (st < NQ) {
-          seg_m[sl * 64 + st] = m_run[st];
-          seg_l[sl * 64 + st] = wred[st] + wred[64 + st] + wred[128 + st] + wred[192 + st];
-        }
-        if (st == 0) {
-          I->seg_u[sl] = iu;
-          I->seg_at[sl] = qc | ((seg_t0 == 0 && t == cs.tb - 1) ? 1 << 30 : 0);
-          I->seg_b[sl] = b;
-          I->seg_h[sl] = cs.h;
-          I->seg_e[sl] = e_ref;
-        }
-        if (sl) end1 = i; else end0 = i;
-        ++n_done;
+        tc::named_bar_sync(bar_a, GT);
       }
-
-      // ---- a finished segment writes its result once its last PV is two tiles back,
-      // and at the latest at the end of the segment after it (the one two on reuses its
-      // O buffer)
-      while (n_fin < n_done) {
-        const int e = (n_fin & 1) ? end1 : end0;
-        if (!(e <= i - 2 || (last && seg == n_fin + 1))) break;
-        if (pv_waited < e) {
-          tc::mbar_wait(&pv_done[e & 1], (uint32_t)(e >> 1) & 1u, abort_flag, p.status);
-          pv_waited = e;
-        }
-        tc::tc_fence_after();
-        finish(n_fin);
-        ++n_fin;
+      const int sl = seg & 1;
+      if (gt < NQ) {
+        seg_m[sl * 128 + grp * 64 + gt] = last >= 0 ? m_run[gt] : kNone;
+        seg_l[sl * 128 + grp * 64 + gt] =
+            last >= 0 ? wred[gt] + wred[64 + gt] + wred[128 + gt] + wred[192 + gt] : 0.f;
       }
-      if (!last) {
-        ++cs.t;
-      } else if (i + 1 < T) {
+      if (gt == 0) {
+        I->seg_has[sl][grp] = last >= 0;
+        I->seg_e[sl][grp] = e_ref;
+        I->seg_bad[sl][grp] = I->bad_run[grp];
+        I->bad_run[grp] = 0;
+      }
+      if constexpr (FP8) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&q_empty[seg & 1]);  // the scales of Q are read
+      }
+      d_seg = seg;
+      int* it = I->item[sl][grp];
+      it[0] = qc;
+      it[1] = b;
+      it[2] = cs.h;
+      it[3] = u0 + i0 - cs.t;
+      it[4] = cs.t == 0 && nt == cs.tb;
+      it[5] = last;
+      d_pub = d_fin = false;
+      i0 += nt;
+      if (i0 < T) {
         cs.next_item(S);
-        len = s_len[cs.b];
-        lim = len + s_nn[cs.b];
         if constexpr (FP8) {
-          sc_head = head_of(cs);
-          load_scales(0);
+          sc_head = ((size_t)cs.b * p.Hkv + cs.h) * p.N;
+          load_scales(KG == 2 ? (i0 ^ grp) & 1 : 0);
         }
       }
     }
 
-    // ---- the segments not yet finished: the last one or two
-    tc::named_bar_sync(1, kSmx);  // their (m, l) and places are in shared memory
-    if (n_fin < n_done) {
-      if (pv_waited < T - 1) {
-        tc::mbar_wait(&pv_done[(T - 1) & 1], (uint32_t)((T - 1) >> 1) & 1u, abort_flag, p.status);
-        pv_waited = T - 1;
-      }
-      tc::tc_fence_after();
-    }
-    while (n_fin < n_done) {
-      finish(n_fin);
-      ++n_fin;
-    }
-    // the finisher has taken the counts of this CTA's partials
-    tc::named_bar_sync(3, kSmx + 32);
+    // ---- the finisher has taken the counts of this CTA's partials
+    tc::named_bar_sync(kBarCount, C::kSmx + 32);
     for (int slot = 0; slot < 2; ++slot) {
       const int iu = I->merge_u[slot];
       if (iu < 0) continue;
       // ---- merge an item whose contributors have all stored their partials, in CTA
-      // order: per column M = max m_j and L = sum 2^(m_j - M) l_j, then
-      // O = sum (2^(m_j - M) / L) O_j.  The tiles' shared memory is idle by now and takes
-      // the contributors' m and weights; every round of loads is issued whole before its
-      // first use.
-      __threadfence();
+      // order: with M the largest m_j, O = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j.  A
+      // thread takes 8 columns of its dh row at a time and folds the contributors in
+      // rounds whose loads are all issued before the first is used: one round trip to L2
+      // a round, and no barrier.  (Read around L1: the finisher's fence and the barrier
+      // above order these loads behind the stores.)
       Cursor at;
       at.init(iu, S);
       const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + at.tb - 1, U, G);
@@ -1182,72 +1302,97 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int sl = (long long)U * cb < iu_g;
         return p.partials + ((size_t)cb * 2 + sl) * C::kPartFloats;
       };
-      float* w_m = reinterpret_cast<float*>(smem);  // [n_c][NQ]: m, then the weights
-      float* w_l = w_m + n_c * NQ;                  // [n_c][NQ]
-      bool bad = false;
-#pragma unroll 4
-      for (int x = st; x < n_c * NQ; x += kSmx) {
-        const int j = x / NQ, c = x - j * NQ;
-        const float* pc = part_of(j) + (size_t)NQ * DH;
-        w_m[x] = __ldcg(pc + c);
-        w_l[x] = __ldcg(pc + NQ + c);
-        if (c == 0) bad |= __ldcg(pc + 2 * NQ) != 0.f;
-      }
-      bad = bar_any(2, kSmx, bad);
-      if (st < NQ) {
-        float M = kNone, L = 0.f;
-        for (int j = 0; j < n_c; ++j) M = fmaxf(M, w_m[j * NQ + st]);
-        for (int j = 0; j < n_c; ++j) L += exp2f(w_m[j * NQ + st] - M) * w_l[j * NQ + st];
-        const float inv = 1.f / L;
-        for (int j = 0; j < n_c; ++j) w_m[j * NQ + st] = exp2f(w_m[j * NQ + st] - M) * inv;
-      }
-      tc::named_bar_sync(1, kSmx);
-      float acc[NQH];
+      constexpr int kJ = 3;  // contributors of a round
+      __nv_bfloat16* o_at = out_of(at.qc, at.b, at.h);
+      const int ncol = columns(at.qc, at.b);
+      const int d_row = kl < DH ? kl : 0;
+      float bad = 0.f;
+#pragma unroll 1
+      for (int f = f0; f < f0 + NF; f += 8) {
+        float M[8], L[8], acc[8];
 #pragma unroll
-      for (int c = 0; c < NQH; ++c) acc[c] = 0.f;
-      if (kl < DH) {
-        constexpr int kJ = 4;  // contributors per round of loads
+        for (int c = 0; c < 8; ++c) {
+          M[c] = kNone;
+          L[c] = acc[c] = 0.f;
+        }
+#pragma unroll 1
         for (int j0 = 0; j0 < n_c; j0 += kJ) {
-          float4 ov[kJ][NQH / 4];
+          float4 m[kJ][2], l4[kJ][2], o[kJ][2];
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             // past the last contributor: its values once more, not used
-            const float4* src = reinterpret_cast<const float4*>(part_of(min(j0 + j, n_c - 1))) +
-                                c0 / 4 * DH + kl;
+            const float* pc = part_of(min(j0 + j, n_c - 1));
+            const float4* ml = reinterpret_cast<const float4*>(pc + (size_t)NQ * DH + f);
+            const float4* ov = reinterpret_cast<const float4*>(pc) + f / 4 * DH + d_row;
 #pragma unroll
-            for (int v = 0; v < NQH / 4; ++v) ov[j][v] = __ldcg(src + v * DH);
+            for (int v = 0; v < 2; ++v) {
+              m[j][v] = __ldcg(ml + v);
+              l4[j][v] = __ldcg(ml + NQ / 4 + v);
+              o[j][v] = __ldcg(ov + v * DH);
+            }
+            bad += __ldcg(pc + (size_t)NQ * DH + 2 * NQ);
           }
 #pragma unroll
           for (int j = 0; j < kJ; ++j) {
             if (j0 + j >= n_c) break;
-            const float4* wj = reinterpret_cast<const float4*>(w_m + (j0 + j) * NQ + c0);
+            const float mj[8] = {m[j][0].x, m[j][0].y, m[j][0].z, m[j][0].w,
+                                 m[j][1].x, m[j][1].y, m[j][1].z, m[j][1].w};
+            const float lj[8] = {l4[j][0].x, l4[j][0].y, l4[j][0].z, l4[j][0].w,
+                                 l4[j][1].x, l4[j][1].y, l4[j][1].z, l4[j][1].w};
+            const float oj[8] = {o[j][0].x, o[j][0].y, o[j][0].z, o[j][0].w,
+                                 o[j][1].x, o[j][1].y, o[j][1].z, o[j][1].w};
 #pragma unroll
-            for (int v = 0; v < NQH / 4; ++v) {
-              const float4 w = wj[v];
-              acc[4 * v] = fmaf(w.x, ov[j][v].x, acc[4 * v]);
-              acc[4 * v + 1] = fmaf(w.y, ov[j][v].y, acc[4 * v + 1]);
-              acc[4 * v + 2] = fmaf(w.z, ov[j][v].z, acc[4 * v + 2]);
-              acc[4 * v + 3] = fmaf(w.w, ov[j][v].w, acc[4 * v + 3]);
+            for (int c = 0; c < 8; ++c) {
+              const float mn = fmaxf(M[c], mj[c]);
+              const float a = ex2_approx(M[c] - mn), w = ex2_approx(mj[c] - mn);
+              L[c] = L[c] * a + w * lj[c];
+              acc[c] = acc[c] * a + w * oj[c];
+              M[c] = mn;
             }
           }
         }
-      }
-      tc::named_bar_sync(1, kSmx);  // the weights are read: the next item may take their place
-      if (kl < DH) {
-        __nv_bfloat16* o_at = out_of(at.qc, at.b, at.h);
-        const int ncol = columns(at.qc, at.b);
+        if (kl < DH) {
 #pragma unroll
-        for (int c = 0; c < NQH; ++c)
-          if (c0 + c < ncol) o_at[col_off[c0 + c]] = __float2bfloat16_rn(acc[c]);
-        if (bad)
-          add_unfit<DH, FP8>(p, at.qc, at.b, at.h, s_len[at.b], s_nn[at.b], c0, c0 + NQH, kl);
+          for (int c = 0; c < 8; ++c)
+            if (f + c < ncol)
+              o_at[col_off[f + c]] = __float2bfloat16_rn(__fdividef(acc[c], L[c]));
+        }
+      }
+      if (bad != 0.f && kl < DH)
+        add_unfit<DH, FP8>(p, at.qc, at.b, at.h, s_len[at.b], s_nn[at.b], f0, f0 + NF, kl);
+    }
+  } else {
+    // ------------------------------------------------------------ Q, finisher
+    // 8 bits: the next items' rows as two e4m3 parts, each into the Q buffer its QKs will
+    // read (the range's first is split by the softmax warps), by warps 2 and 3.  Then
+    // warp 2, for each partial of this CTA: wait until the softmax warps have issued its
+    // stores, make them visible device-wide, count this contributor in.  The last of an
+    // item's contributors merges it, after its range.
+    if constexpr (FP8) {
+      int* w_max = reinterpret_cast<int*>(qsc) + 18;  // [2 buffers][2 warps]
+      Cursor cq;
+      cq.init(u0, S);
+      int left = T - (cq.tb - cq.t);
+      for (int n = 1; left > 0; ++n) {
+        const int qb = n & 1;
+        cq.next_item(S);
+        tc::mbar_wait(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status);
+        const float unit = split_q<NQ, DH, 2>(
+            p, cq.qc, cq.b, cq.h, s_nn[cq.b], warp - 2, q_buf + qb * C::kQParts * C::kQPart,
+            [&](uint32_t mx) {
+              // (read by both before either can write this buffer's again: two rounds on)
+              if (lane == 0) w_max[2 * qb + warp - 2] = (int)mx;
+              tc::named_bar_sync(7, 64);
+              return (uint32_t)max(w_max[2 * qb], w_max[2 * qb + 1]);
+            });
+        if (warp == 2 && lane == 0) qsc[qb] = unit;
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&q_full[qb]);
+        left -= cq.tb;
       }
     }
-  } else if (warp == C::kFinisher) {
-    // ------------------------------------------------------------ finisher
-    // For each partial of this CTA: wait until the softmax warps have issued its
-    // stores, make them visible device-wide, count this contributor in.  The last of
-    // an item's contributors merges it, after its range.
+    if (warp == C::kFinisher) {
     if (lane == 0) {
       I->merge_u[0] = -1;
       I->merge_u[1] = -1;
@@ -1262,40 +1407,24 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         bool ready = false;
         IdleClock clk;
         while (!(ready = tc::mbar_test(&fin_full[slot], 0u))) {
-          __nanosleep(256);
+          __nanosleep(64);
           if (!clk.idle(abort_flag, p.status)) break;
         }
         if (!ready) break;
-        __threadfence();
+        fence_gpu();
         const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + tb - 1, U, G);
         // an item that goes on behind CTA c_first's range is the only one to do so, so
         // c_first names its counter
         const unsigned prev = atomicAdd(&p.cnt[c_first], 1u);
         if (prev == (unsigned)(c_last - c_first)) {
+          fence_gpu();
           p.cnt[c_first] = 0u;  // for the next call
           I->merge_u[slot] = iu;
         }
       }
     }
     __syncwarp();
-    tc::named_bar_sync(3, kSmx + 32);
-  } else if constexpr (FP8) {
-    // ------------------------------------------------------------ Q splitter
-    // The next item's rows as two e4m3 parts, into the Q buffer its QKs will read.
-    // (the first is split by the softmax warps)
-    Cursor cq;
-    cq.init(u0, S);
-    int left = T - (cq.tb - cq.t);
-    for (int n = 1; left > 0; ++n) {
-      const int qb = n & 1;
-      cq.next_item(S);
-      tc::mbar_wait(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status);
-      split_q<NQ, DH>(p, cq.qc, cq.b, cq.h, s_nn[cq.b], 0, 1, q_buf + qb * C::kQParts * C::kQPart,
-                      qsc + qb * 64);
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&q_full[qb]);
-      left -= cq.tb;
+    tc::named_bar_sync(5, kSmx + 32);
     }
   }
 
@@ -1309,22 +1438,25 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 struct TreePlan {
-  int NQ, tn, n_qc, nk, nv, grid;
+  int NQ, tn, gs, hs, n_qc, nk, nv, grid;
   size_t smem_bytes;
 };
 
 // Rows of an item: the smallest instance that takes them all, else chunks of 64 (of
-// whole nodes).  A 16-column P of one byte has no swizzled layout, and 24 columns a
-// thread no whole 16-byte chunks: 8 bits run at 32 and 64.
+// whole nodes).  8 bits: chunks of 32.  (16 columns of one-byte P have no swizzled
+// layout; at 64 one group of 16 warps took 5000 cycles a tile against 2 x 1400 for two
+// chunks of 32.)
 TreePlan plan(const TreeAttnArgs& a, int num_sms) {
   TreePlan q{};
   const int g = a.Hq / a.Hkv, rows = a.T * g;
   if (a.fp8)
-    q.NQ = rows <= 32 ? 32 : 64;
+    q.NQ = 32;
   else
     q.NQ = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 48 ? 48 : 64));
-  q.tn = q.NQ / g < a.T ? q.NQ / g : a.T;
-  q.n_qc = (a.T + q.tn - 1) / q.tn;
+  q.hs = g > q.NQ ? 2 : 1;
+  q.gs = (g + q.hs - 1) / q.hs;
+  q.tn = q.NQ / q.gs < a.T ? q.NQ / q.gs : a.T;
+  q.n_qc = (a.T + q.tn - 1) / q.tn * q.hs;
   const long long units = (long long)a.B * a.Hkv * q.n_qc * ((a.N + kKT - 1) / kKT);
   q.grid = (int)(units < num_sms ? units : num_sms);
   const size_t boxes = a.fp8 ? 1 : a.dh / 64, elt = a.fp8 ? 1 : 2;
@@ -1332,8 +1464,9 @@ TreePlan plan(const TreeAttnArgs& a, int num_sms) {
   const size_t nqp = q.NQ == 48 ? 64 : q.NQ;
   size_t qbytes = a.fp8 ? (size_t)4 * q.NQ * a.dh : boxes * q.NQ * 128;
   qbytes = align_up(qbytes, 1024);
-  const size_t pbytes = 2 * (a.fp8 ? 3 : 1) * kKT * nqp * elt;
-  const size_t misc = align_up((size_t)Misc::kSeq + (3 * (size_t)a.B + 1) * 4, 16);
+  const size_t pbytes = 2 * kKT * (a.fp8 ? 128 : nqp * 2);
+  const size_t misc = Misc::kBytes + Misc::seq_bytes(a.B) +
+                      (a.fp8 ? Cfg<32, 128, true>::kSmx * sizeof(float2) : 0);
   const size_t fixed = 1024 + qbytes + pbytes + misc;
   int tiles = (int)((kSmemBudget - fixed) / tile);
   if (tiles > 16) tiles = 16;
@@ -1341,8 +1474,6 @@ TreePlan plan(const TreeAttnArgs& a, int num_sms) {
   q.nv = (tiles + 1) / 2;
   q.nk = tiles - q.nv;
   q.smem_bytes = fixed + (size_t)tiles * tile;
-  // a merge keeps two floats a row of every contributor where the tiles were
-  if ((size_t)q.grid * q.NQ * 8 > (size_t)tiles * tile) q.grid = (int)(tiles * tile / (q.NQ * 8));
   return q;
 }
 
@@ -1377,8 +1508,7 @@ size_t tree_tc_workspace_bytes(int Hq, int Hkv, int dh, int T, int num_sms) {
   // the larger of the two cache forms
   const int rows = T * (Hq / Hkv);
   const int NQ = rows <= 32 ? 32 : (rows <= 48 ? 48 : 64);
-  const int NQ8 = rows <= 32 ? 32 : 64;
-  const size_t floats = part_floats(NQ > NQ8 ? NQ : NQ8, dh);
+  const size_t floats = part_floats(NQ, dh);
   return kMaxGrid * sizeof(unsigned) + align_up((size_t)num_sms * 2 * floats * sizeof(float), 256);
 }
 
@@ -1417,7 +1547,7 @@ cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream) {
   if (a.fp8) maps[0] = maps[1];  // not read
   TreeParams prm{};
   prm.B = a.B; prm.N = a.N; prm.Hq = a.Hq; prm.Hkv = a.Hkv; prm.g = (int)g; prm.T = a.T;
-  prm.n_qc = q.n_qc; prm.tn = q.tn; prm.nk = q.nk; prm.nv = q.nv;
+  prm.n_qc = q.n_qc; prm.tn = q.tn; prm.gs = q.gs; prm.hs = q.hs; prm.nk = q.nk; prm.nv = q.nv;
   prm.keep = q.n_qc > 1;
   prm.qk_scale = kLog2e / sqrtf((float)a.dh);
   prm.q = a.q; prm.v_cache = a.v_cache; prm.k_scale = a.k_scale; prm.v_scale = a.v_scale;
@@ -1437,9 +1567,7 @@ cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream) {
   FDLLM_TREE_CASE(48, 128, false)
   FDLLM_TREE_CASE(64, 128, false)
   FDLLM_TREE_CASE(32, 64, true)
-  FDLLM_TREE_CASE(64, 64, true)
   FDLLM_TREE_CASE(32, 128, true)
-  FDLLM_TREE_CASE(64, 128, true)
 #undef FDLLM_TREE_CASE
   return cudaErrorInvalidValue;
 }

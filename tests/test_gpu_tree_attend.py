@@ -6,8 +6,9 @@ S = max_s sum_d |q_d k_sd| / sqrt(dh):
            1 + that on each weight, twice (weight and normaliser); 2^-21 more for exp2
   sums     n terms in fp32, rescaled as the maximum rises: n 2^-23
   weights  rounded to bf16 for the tensor cores (16- and 8-bit caches): 2^-8
-  queries  kept as two e4m3 parts for an 8-bit cache: each off by at most 2^-18 of the
-           row's largest, i.e. dh 2^-18 max|q| max|k| / sqrt(dh) on a score
+  queries  kept as two e4m3 parts for an 8-bit cache: off by at most half the second
+           part's smallest step, 2^-10 where the largest of the rows that share a kv head
+           is at least 128, i.e. 2^-17 of it: dh 2^-17 max|q| max|k| / sqrt(dh) on a score
   output   rounded to bf16 (2^-8 of it) or fp32 (2^-24)
 """
 import numpy as np
@@ -102,9 +103,10 @@ class Case:
             out, A, S = O.tree_attend(q64[b], self.k64[b], self.v64[b], L, par, n)
             e = 2 * ((self.dh + 10) * 2.0 ** -24 * S + 2.0 ** -21) + (L + n) * 2.0 ** -23
             if self.kind == "fp8":
-                qm = np.abs(q64[b, :n]).max(-1)
-                km = np.nanmax(np.abs(self.k64[b, :, :L + n]), (1, 2)).repeat(self.Hq // self.Hkv)
-                e = e + 2 * np.sqrt(self.dh) * 2.0 ** -18 * qm * km
+                g = self.Hq // self.Hkv
+                qm = np.abs(q64[b, :n]).reshape(n, self.Hkv, g * self.dh).max((0, 2)).repeat(g)
+                km = np.nanmax(np.abs(self.k64[b, :, :L + n]), (1, 2)).repeat(g)
+                e = e + 2 * np.sqrt(self.dh) * 2.0 ** -17 * qm * km
             if self.kind != "f32":
                 e = e + 2.0 ** -8
             half = 2.0 ** -24 if self.kind == "f32" else 2.0 ** -8
