@@ -51,7 +51,28 @@ def _stream(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, device):
+    """_stream for calls whose host time counts: the current stream's handle, without the
+    2 us that a torch.cuda.Stream object takes, where there is nothing to refuse."""
+    if stream is None and _raw_stream is not None and device.index == torch.cuda.current_device():
+        return _raw_stream(device.index)
+    return _stream(stream, device)
+
+
+def _at(t):
+    """The address of a tensor's data, None for no tensor."""
+    return None if t is None else t.data_ptr()
+
+
 def _need(t, name, dtype=None, shape=None, device=None):
+    # one look at a tensor that fits (torch.Size compares with tuples); the cause otherwise
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()
+            and (dtype is None or t.dtype == dtype) and (shape is None or t.shape == shape)
+            and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -368,10 +389,10 @@ def fdllm_cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scal
     k_rows, v_rows [B, R, H, dh]; pos int32 [B, R], -1 skips a row; the caches
     float8_e4m3fn [B, H, N, dh] with float32 scales [B, H, N], updated in place."""
     B, N, H, dh, R = _check_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
-    st = lib().fdllm_cache_write_fp8(B, N, H, dh, R, _dtype_code(k_rows), _p(k_rows), _p(v_rows),
-                                     _p(pos), _p(k_cache), _p(v_cache), _p(k_scale), _p(v_scale),
-                                     _p(workspace), workspace.numel(),
-                                     _stream(stream, k_rows.device))
+    st = lib().fdllm_cache_write_fp8(B, N, H, dh, R, _dtype_code(k_rows), _at(k_rows), _at(v_rows),
+                                     _at(pos), _at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale),
+                                     _at(workspace), workspace.numel(),
+                                     _stream_on(stream, k_rows.device))
     _check(st, "fdllm_cache_write_fp8")
 
 
@@ -379,10 +400,10 @@ def fdllm_cache_read_fp8(pos, k_cache, v_cache, k_scale, v_scale, k_rows, v_rows
                          stream=None):
     """Rows of an 8-bit cache read back into k_rows, v_rows [B, R, H, dh] (see include/fdllm.h)."""
     B, N, H, dh, R = _check_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
-    st = lib().fdllm_cache_read_fp8(B, N, H, dh, R, _dtype_code(k_rows), _p(pos), _p(k_cache),
-                                    _p(v_cache), _p(k_scale), _p(v_scale), _p(k_rows), _p(v_rows),
-                                    _p(workspace), workspace.numel(),
-                                    _stream(stream, k_rows.device))
+    st = lib().fdllm_cache_read_fp8(B, N, H, dh, R, _dtype_code(k_rows), _at(pos), _at(k_cache),
+                                    _at(v_cache), _at(k_scale), _at(v_scale), _at(k_rows), _at(v_rows),
+                                    _at(workspace), workspace.numel(),
+                                    _stream_on(stream, k_rows.device))
     _check(st, "fdllm_cache_read_fp8")
     return k_rows, v_rows
 
@@ -415,9 +436,9 @@ def fdllm_tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, work
     [B, T] or None (a chain); n_nodes int32 [B] or None (T); out [B, T, Hq*dh]."""
     B, N, Hq, Hkv, dh, T = _check_tree(q, k_cache, v_cache, q.dtype, cache_len, parent, n_nodes,
                                        out, workspace)
-    st = lib().fdllm_tree_attend(B, N, Hq, Hkv, dh, T, _dtype_code(q), _p(q), _p(k_cache),
-                                 _p(v_cache), _p(cache_len), _p(parent), _p(n_nodes), _p(out),
-                                 _p(workspace), workspace.numel(), _stream(stream, q.device))
+    st = lib().fdllm_tree_attend(B, N, Hq, Hkv, dh, T, _dtype_code(q), _at(q), _at(k_cache),
+                                 _at(v_cache), _at(cache_len), _at(parent), _at(n_nodes), _at(out),
+                                 _at(workspace), workspace.numel(), _stream_on(stream, q.device))
     _check(st, "fdllm_tree_attend")
     return out
 
@@ -429,10 +450,10 @@ def fdllm_tree_attend_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_len, pare
                                        n_nodes, out, workspace)
     _need(k_scale, "k_scale", torch.float32, (B, Hkv, N), q.device)
     _need(v_scale, "v_scale", torch.float32, (B, Hkv, N), q.device)
-    st = lib().fdllm_tree_attend_fp8(B, N, Hq, Hkv, dh, T, _dtype_code(q), _p(q), _p(k_cache),
-                                     _p(v_cache), _p(k_scale), _p(v_scale), _p(cache_len),
-                                     _p(parent), _p(n_nodes), _p(out), _p(workspace),
-                                     workspace.numel(), _stream(stream, q.device))
+    st = lib().fdllm_tree_attend_fp8(B, N, Hq, Hkv, dh, T, _dtype_code(q), _at(q), _at(k_cache),
+                                     _at(v_cache), _at(k_scale), _at(v_scale), _at(cache_len),
+                                     _at(parent), _at(n_nodes), _at(out), _at(workspace),
+                                     workspace.numel(), _stream_on(stream, q.device))
     _check(st, "fdllm_tree_attend_fp8")
     return out
 
@@ -460,9 +481,9 @@ def fdllm_chain_verify(target, draft, tok, n_draft, u, r, n_accept, next_tok, wo
     _need(n_accept, "n_accept", torch.int32, (B,), dev)
     _need(next_tok, "next_tok", torch.int32, (B,), dev)
     _need(workspace, "workspace", torch.uint8, None, dev)
-    st = lib().fdllm_chain_verify(B, T, V, _p(target), _p(draft), _p(tok), _p(n_draft), _p(u),
-                                  _p(r), _p(n_accept), _p(next_tok), _p(workspace),
-                                  workspace.numel(), _stream(stream, dev))
+    st = lib().fdllm_chain_verify(B, T, V, _at(target), _at(draft), _at(tok), _at(n_draft), _at(u),
+                                  _at(r), _at(n_accept), _at(next_tok), _at(workspace),
+                                  workspace.numel(), _stream_on(stream, dev))
     _check(st, "fdllm_chain_verify")
     return n_accept, next_tok
 
@@ -488,9 +509,9 @@ def fdllm_tree_verify(target, tok, parent, n_nodes, u, r, path, n_accept, next_t
     _need(n_accept, "n_accept", torch.int32, (B,), dev)
     _need(next_tok, "next_tok", torch.int32, (B,), dev)
     _need(workspace, "workspace", torch.uint8, None, dev)
-    st = lib().fdllm_tree_verify(B, T, V, _p(target), _p(tok), _p(parent), _p(n_nodes), _p(u),
-                                 _p(r), _p(path), _p(n_accept), _p(next_tok), _p(workspace),
-                                 workspace.numel(), _stream(stream, dev))
+    st = lib().fdllm_tree_verify(B, T, V, _at(target), _at(tok), _at(parent), _at(n_nodes), _at(u),
+                                 _at(r), _at(path), _at(n_accept), _at(next_tok), _at(workspace),
+                                 workspace.numel(), _stream_on(stream, dev))
     _check(st, "fdllm_tree_verify")
     return path, n_accept, next_tok
 

@@ -49,6 +49,8 @@
 // outputs of those that do when they are written.
 #include <limits.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
@@ -1479,13 +1481,27 @@ TreePlan plan(const TreeAttnArgs& a, int num_sms) {
 
 size_t part_floats(int NQ, int dh) { return (size_t)NQ * dh + 2 * NQ + 4; }
 
+// Raises a kernel's shared-memory limit, once a device (a bit of `done`; setting it twice
+// does no harm).
+cudaError_t allow_smem(const void* kern, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+template <int NQ, int DH, bool FP8>
+std::atomic<unsigned long long> raised{0};
+
 template <int NQ, int DH, bool FP8>
 cudaError_t launch_t(const TreePlan& q, TreeParams prm, const CUtensorMap* maps,
                      cudaStream_t stream) {
   using C = Cfg<NQ, DH, FP8>;
   auto kern = tree_tc_kernel<NQ, DH, FP8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)q.smem_bytes);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), &raised<NQ, DH, FP8>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(q.grid);
