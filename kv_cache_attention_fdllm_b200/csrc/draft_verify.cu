@@ -17,7 +17,7 @@
 // Bound: HBM over one row pair (tree: one row) a sequence, and latency below some
 // tens of sequences.  One launch: every CTA of a sequence walks its drafts itself
 // (all gathers at once, then shared memory), which costs less than a second
-// launch; its warps then sum sub-blocks of 1024 weights, 16-byte loads all in
+// launch; its warps then sum sub-blocks of 512 weights, 16-byte loads all in
 // flight before the first is used; the last CTA of the sequence to finish finds
 // the sub-block that holds r sum(w) from the sums, and in it the token.
 #include <limits.h>
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSub = 1024;  // weights of one partial sum: 8 x 4 a lane
+constexpr int kSub = 512;  // weights of one partial sum: 4 x 4 a lane
 constexpr int kMaxNodes = FDLLM_MAX_TREE_NODES;
 
 // A child's tokens are left out of a tree's draw: at most kMaxNodes - 1 of them.
@@ -89,21 +89,17 @@ __device__ __forceinline__ double warp_sum(double v) {
 // Sum of sub-block s by one warp.
 __device__ __forceinline__ double sub_sum(const Weights& w, int s, const int* out, int n_out,
                                           int lane) {
-  float4 p[8], q[8];
+  const int i0 = s * kSub + lane * 4;
+  float4 p[4], q[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) load4(w, s * kSub + k * 128 + lane * 4, &p[k], &q[k]);
+  for (int k = 0; k < 4; ++k) load4(w, i0 + k * 128, &p[k], &q[k]);
   if (n_out) {
-    for (int k = 0; k < n_out; ++k) {
-      const int e = out[k] - s * kSub;
-      if (e < 0 || e >= kSub || ((e >> 2) & 31) != lane) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j == (e >> 7)) leave_out(out + k, 1, s * kSub + j * 128 + lane * 4, &p[j]);
-    }
+    for (int k = 0; k < 4; ++k) leave_out(out, n_out, i0 + k * 128, &p[k]);
   }
   double t = 0.0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) t += sum4(p[k], q[k]);
+  for (int k = 0; k < 4; ++k) t += sum4(p[k], q[k]);
   return warp_sum(t);
 }
 
@@ -144,17 +140,18 @@ __device__ int draw(const Weights& w, const double* parts, int n_sub, float r, c
                     int n_out, Scan& sh, Pick& pk) {
   const int tid = threadIdx.x;
   const double rr = (double)fminf(fmaxf(r, 0.f), 0.99999994f);
-  double total = 0.0;
+  // the running sums (of the one round of threads that a vocabulary usually needs, kept)
+  double total = 0.0, x = 0.0, c = 0.0;
   for (int s0 = 0; s0 < n_sub; s0 += kThreads) {
+    x = s0 + tid < n_sub ? __ldcg(parts + s0 + tid) : 0.0;
     double t;
-    block_scan(s0 + tid < n_sub ? __ldcg(parts + s0 + tid) : 0.0, sh, &t);
+    c = total + block_scan(x, sh, &t);
     total += t;
   }
   if (!(total > 0.0)) return -1;
   const double want = rr * total;
   // the first sub-block whose running sum exceeds it; the last with any weight
   // where rounding leaves none
-  __syncthreads();
   if (tid == 0) {
     pk.best = INT_MAX;
     pk.last = -1;
@@ -163,14 +160,16 @@ __device__ int draw(const Weights& w, const double* parts, int n_sub, float r, c
   __syncthreads();
   double base = 0.0;
   for (int s0 = 0; s0 < n_sub; s0 += kThreads) {
-    const double x = s0 + tid < n_sub ? __ldcg(parts + s0 + tid) : 0.0;
-    double t;
-    const double c = base + block_scan(x, sh, &t);
+    if (n_sub > kThreads) {
+      x = s0 + tid < n_sub ? __ldcg(parts + s0 + tid) : 0.0;
+      double t;
+      c = base + block_scan(x, sh, &t);
+      base += t;
+    }
     if (x > 0.0 && c > want) atomicMin(&pk.best, s0 + tid);
     if (x > 0.0) atomicMax(&pk.last, s0 + tid);
     __syncthreads();
     if (pk.best == s0 + tid || (pk.best == INT_MAX && pk.last == s0 + tid)) pk.base = c - x;
-    base += t;
     __syncthreads();
     if (pk.best != INT_MAX) break;
   }
@@ -181,19 +180,24 @@ __device__ int draw(const Weights& w, const double* parts, int n_sub, float r, c
     pk.best = INT_MAX;
     pk.last = -1;
   }
-  // its weights, 4 a thread in order
-  const int i = sub * kSub + tid * 4;
-  float4 p, q;
-  load4(w, i, &p, &q);
-  leave_out(out, n_out, i, &p);
-  const double x[4] = {weight(p.x, q.x), weight(p.y, q.y), weight(p.z, q.z), weight(p.w, q.w)};
-  const double four = (x[0] + x[1]) + (x[2] + x[3]);
-  double t;
-  double c = base + block_scan(four, sh, &t) - four;
+  // its weights, 2 a thread in order
+  static_assert(kSub == 2 * kThreads, "two weights a thread");
+  const int i = sub * kSub + tid * 2;
+  double y[2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    c += x[e];
-    if (x[e] > 0.0) {
+  for (int e = 0; e < 2; ++e) {
+    float p = i + e < w.V ? __ldg(w.p + i + e) : 0.f;
+    const float q = w.q && i + e < w.V ? __ldg(w.q + i + e) : 0.f;
+    for (int k = 0; k < n_out; ++k)
+      if (out[k] == i + e) p = 0.f;
+    y[e] = weight(p, q);
+  }
+  double t;
+  c = base + block_scan(y[0] + y[1], sh, &t) - (y[0] + y[1]);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    c += y[e];
+    if (y[e] > 0.0) {
       if (c > want) atomicMin(&pk.best, i + e);
       atomicMax(&pk.last, i + e);
     }
@@ -204,7 +208,7 @@ __device__ int draw(const Weights& w, const double* parts, int n_sub, float r, c
 
 // grid B * ctas: `ctas` CTAs a sequence
 template <bool TREE>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(DraftVerifyArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(DraftVerifyArgs a, int ctas) {
   const int b = blockIdx.x / ctas, cta = blockIdx.x - b * ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int T = a.T, V = a.V;
@@ -226,9 +230,8 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(DraftVerifyArgs 
 
   // ---- the walk
   if constexpr (TREE) {
-    __shared__ int s_par[kMaxNodes], s_tok[kMaxNodes], s_choice[kMaxNodes];
+    __shared__ int s_par[kMaxNodes], s_tok[kMaxNodes], s_path[kMaxNodes];
     __shared__ float s_w[kMaxNodes], s_u[kMaxNodes];
-    __shared__ bool s_twin[kMaxNodes];
     static_assert(kMaxNodes <= kThreads, "one thread a node");
     int par = -1, tk = 0;
     if (tid < n) {
@@ -243,38 +246,51 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(DraftVerifyArgs 
           s_w[tid] = a.target[((size_t)b * T + par) * V + tk];
         }
       }
-      s_par[tid] = par;
       s_tok[tid] = tk;
-      s_choice[tid] = INT_MAX;
     }
+    if (tid < kMaxNodes) s_par[tid] = par;
     __syncthreads();
-    if (par >= 0) {
-      bool twin = false;
-      for (int s = 1; s < tid; ++s) twin |= s_par[s] == par && s_tok[s] == tk;
-      s_twin[tid] = twin;
-    }
-    __syncthreads();
-    if (par >= 0 && !s_twin[tid]) {
-      double c = 0.0;
-      for (int s = 1; s <= tid; ++s)
-        if (s_par[s] == par && !s_twin[s]) c += fmax((double)s_w[s], 0.0);
-      if ((double)s_u[par] < c) atomicMin(&s_choice[par], tid);
-    }
-    __syncthreads();
-    if (tid == 0) {
+    if (warp == 0) {
+      // one warp walks: the children of the node are a ballot over 32 nodes at a time,
+      // taken in order until the running sum exceeds the node's number
       int node = 0, len = 0;
-      while (s_choice[node] != INT_MAX) {
-        node = s_choice[node];
-        s_w[len++] = __int_as_float(node);  // the weights are used up
+      for (int next = 0; next >= 0;) {
+        const double un = (double)s_u[node];
+        double c = 0.0;
+        next = -1;
+        for (int k = 0; k < n && next < 0; k += 32) {
+          unsigned kids = __ballot_sync(0xffffffffu, s_par[k + lane] == node);
+          while (kids && next < 0) {
+            const int j = k + __ffs(kids) - 1;
+            c += fmax((double)s_w[j], 0.0);
+            if (un < c) next = j;
+            // siblings behind it that repeat its token add nothing: out of the tree
+            const int x = s_tok[j];
+            __syncwarp();
+            for (int m = k; m < n; m += 32) {
+              const int t = m + lane;
+              if (t > j && s_par[t] == node && s_tok[t] == x) s_par[t] = -1;
+            }
+            __syncwarp();
+            kids = __ballot_sync(0xffffffffu, s_par[k + lane] == node && k + lane > j);
+          }
+        }
+        if (next >= 0) {
+          if (lane == 0) s_path[len] = next;
+          ++len;
+          node = next;
+        }
       }
-      s_node = node;
-      s_len = len;
+      if (lane == 0) {
+        s_node = node;
+        s_len = len;
+      }
     }
     __syncthreads();
     if (par == s_node) s_out[atomicAdd(&s_n_out, 1)] = tk;
     if (first_cta)
       for (int t = tid; t < T; t += kThreads)
-        a.path[(size_t)b * T + t] = t < s_len ? __float_as_int(s_w[t]) : -1;
+        a.path[(size_t)b * T + t] = t < s_len ? s_path[t] : -1;
   } else {
     if (tid == 0) s_node = n;
     __syncthreads();
@@ -341,12 +357,13 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(DraftVerifyArgs 
   }
 }
 
-// CTAs of a sequence: about two a SM over all of them, no more than one round of
-// sub-blocks each.
+// CTAs of a sequence: four a SM over all of them, which is what is resident (one CTA more
+// a sequence and the last start when the first end: 20.6 us in place of 17.8 for 64 chains
+// of 4 drafts over 126464 tokens), no more than one round of sub-blocks each.
 int ctas_per_seq(int B, int V) {
   const int n_sub = (V + kSub - 1) / kSub;
   const int most = (n_sub + kWarps - 1) / kWarps;
-  int n = (2 * device_sm_count() + B - 1) / B;
+  int n = 4 * device_sm_count() / B;
   return n < 1 ? 1 : (n > most ? most : n);
 }
 
