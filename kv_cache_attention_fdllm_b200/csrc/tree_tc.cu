@@ -34,14 +34,19 @@
 // last of its contributors (a counter, nobody waits) merges them in CTA order, so
 // results do not depend on timing.
 //
-//   warp 0      TMA producer: K and V tiles, and the rows' Q (16-bit cache)
+//   warp 0      producer: K and V tiles by TMA, with the rows' Q (16 bits) or the slots'
+//               scales (8 bits)
 //   warp 1      TMEM; lane 0 issues both products
-//   warp 2      finisher: counts the partials in; 8 bits: splits the next item's Q into
-//               its two e4m3 parts
+//   warp 2      finisher: counts the partials in; 8 bits: with warp 3 splits the next
+//               item's Q into its two e4m3 parts
 //   warps 4..   softmax (one group, or two that take turns at the tiles), epilogue, merges
 //
 // O^T is double-buffered in TMEM (once for each group): an item's result is written
 // some tiles into the next item, off the softmax path.
+//
+// Instructions are the other bound in 8 bits: what a CTA does once a segment (open, close,
+// merge, write) runs from cold instruction caches, so rare and once-a-segment code is kept
+// out of line and short there.  In 16 bits the same calls cost single tokens 2 us of 22.
 //
 // NaN and infinity.  Slots past the sequence's nodes are masked in S and zeroed in V
 // (0 x NaN would be NaN).  A node's V that is not finite is zeroed the same way, since
@@ -62,11 +67,11 @@ namespace {
 
 constexpr int kKT = 128;  // slots of a tile
 constexpr int kMaxNodes = FDLLM_MAX_TREE_NODES;
-constexpr int kAncWords = kMaxNodes / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -3.0e38f;  // maximum of a row that has seen no slot yet (finite: a
                                    // masked score, -inf, then weighs 2^-inf = 0, not NaN)
 constexpr int kMaxGrid = 1024;     // counters: one a CTA
+constexpr uint32_t kFull = 0xffffffffu;
 constexpr size_t kSmemBudget = 227 * 1024;
 
 struct TreeParams {
@@ -136,12 +141,12 @@ struct Misc {
   static constexpr int kM = 640;                // by group: m_run[64], alpha[64], alpha_o[64]
   static constexpr int kRed = kM + 2 * 768;     // by group: wred[4][64]
   static constexpr int kSegM = kRed + 2 * 1024; // seg_m, seg_l [2 O buffers][2 groups][64]
-  static constexpr int kCol = kSegM + 2 * 1024; // col_node[64] (bytes), col_off[64] (ints)
-  static constexpr int kQsc = kCol + 320;       // qsc[2], maxima of Q by warp [16], [2][2]
+  static constexpr int kCol = kSegM + 2 * 1024; // col_off[64]: a row's offset in q and out
+  static constexpr int kQsc = kCol + 256;       // qsc[2], maxima of Q by warp [16], [2]
   static constexpr int kZero = kQsc + 128;      // [64] zeros
   static constexpr int kPar = kZero + 256;      // by group: parents of a sequence's nodes
-  static constexpr int kAnc = kPar + 2 * kMaxNodes * 4;       // by group: anc[64][kAncWords]
-  static constexpr int kBytes = (kAnc + 2 * 64 * kAncWords * 4 + 1023) / 1024 * 1024;
+  static constexpr int kVis = kPar + 2 * kMaxNodes * 4;  // by group: columns that see a node
+  static constexpr int kBytes = (kVis + 2 * kMaxNodes * 8 + 1023) / 1024 * 1024;
   // of pre[B + 1], len[B], nn[B]
   __host__ __device__ static constexpr int seq_bytes(int B) { return ((3 * B + 1) * 4 + 15) / 16 * 16; }
 };
@@ -230,13 +235,14 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
       : "r"(h));
   return f;
 }
-// one float into shared memory, asynchronously; and the wait for all of the thread's
+// one float into shared memory, asynchronously; an arrival on a barrier when all of the
+// thread's are there
 __device__ __forceinline__ void copy_async4(float* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src)
                : "memory");
 }
-__device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+__device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 // byte offset `off` of a tile whose rows have `row` bytes (32, 64 or 128), swizzled
 __device__ __forceinline__ uint32_t swz(uint32_t off, uint32_t row) {
@@ -282,24 +288,21 @@ __device__ __noinline__ void add_unfit(const TreeParams& p, int qc, int b, int h
   }
 }
 
-// A chunk's Q (bf16) as two e4m3 parts: q 2^sh = q1 + q2 with the chunk's largest in
-// [128, 256), so that what is lost is below 2^-18 of it.  Rows past the sequence's nodes
-// become zeros.  Warp w of W takes every W-th row, all its loads in flight together;
-// `share`: the maximum over the warps.  Returns 2^-sh.
+// A chunk's Q (bf16; `q`: its first row, the others at col_off, ncol in all) as two e4m3
+// parts: q 2^sh = q1 + q2 with the chunk's largest in [128, 256), so that what is lost is
+// below 2^-17 of it.  Rows past ncol become zeros.  Warp w of W takes every W-th row, up to
+// 16 rows' loads in flight together; `share`: the maximum over the warps.  Returns 2^-sh.
 template <int NQ, int DH, int W, typename Share>
-__device__ __forceinline__ float split_q(const TreeParams& p, int qc, int b, int h, int nn, int w,
+__device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_off, int ncol, int w,
                                          uint8_t* dst, Share share) {
   constexpr int R = NQ / W;   // rows of a warp
   constexpr int E = DH / 32;  // elements of a lane
   constexpr uint32_t kPart = NQ * DH;
   const int lane = threadIdx.x & 31;
-  const int rows = p.tn * p.gs, h0 = qc % p.hs * p.gs;
   auto load = [&](int r) {
     uint2 raw = make_uint2(0u, 0u);
-    const int node = qc / p.hs * p.tn + r / p.gs, hd = h0 + r % p.gs;
-    if (r < rows && node < nn && hd < p.g) {
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                 (((size_t)b * p.T + node) * p.Hq + h * p.g + hd) * DH + lane * E;
+    if (r < ncol) {
+      const __nv_bfloat16* src = q + col_off[r] + lane * E;
       if constexpr (E == 4)
         raw = *reinterpret_cast<const uint2*>(src);
       else
@@ -307,72 +310,177 @@ __device__ __forceinline__ float split_q(const TreeParams& p, int qc, int b, int
     }
     return raw;
   };
-  // the largest finite |q|, as the upper 16 bits of a float: bf16 magnitudes compare as
-  // whole numbers
-  uint2 raw[R];
+  // at most 16 rows in registers: a warp's other rows are read twice
+  constexpr int N = R < 16 ? R : 16;
+  uint2 raw[N];
+  uint32_t m2 = 0u;  // two maxima
+#pragma unroll 1
+  for (int x0 = R - N; x0 >= 0; x0 -= N) {
 #pragma unroll
-  for (int x = 0; x < R; ++x) raw[x] = load(w + x * W);
-  uint32_t mx = 0u;
+    for (int x = 0; x < N; ++x) raw[x] = load(w + (x0 + x) * W);
 #pragma unroll
-  for (int x = 0; x < R; ++x) {
-    const uint32_t a[4] = {raw[x].x & 0x7fffu, (raw[x].x >> 16) & 0x7fffu, raw[x].y & 0x7fffu,
-                           (raw[x].y >> 16) & 0x7fffu};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (a[e] < 0x7f80u) mx = max(mx, a[e]);
+    for (int x = 0; x < N; ++x)
+      m2 = __vmaxu2(m2, __vmaxu2(raw[x].x & 0x7fff7fffu, raw[x].y & 0x7fff7fffu));
   }
-  mx = share(__reduce_max_sync(0xffffffffu, mx));
+  // the largest |q| as the upper 16 bits of a float: magnitudes compare as whole numbers,
+  // what is not finite above all the others, which then are looked at once more
+  uint32_t mx = share(__reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16)));
+  const bool odd = mx >= 0x7f80u;
+  if (odd) {
+    mx = 0u;
+    for (int r = w; r < NQ; r += W) {
+      const uint2 v = load(r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a = ((e < 2 ? v.x : v.y) >> (16 * (e & 1))) & 0x7fffu;
+        if (a < 0x7f80u) mx = max(mx, a);
+      }
+    }
+    mx = share(__reduce_max_sync(0xffffffffu, mx));
+  }
   int sh = 7 - ((int)(mx >> 7) - 127);
   sh = mx == 0u ? 0 : min(max(sh, -120), 120);
   const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll 1
+  for (int x0 = 0; x0 < R; x0 += N) {
+    if (x0) {
 #pragma unroll
-  for (int x = 0; x < R; ++x) {
-    const int r = w + x * W;
-    uint32_t b1 = 0u, b2 = 0u;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const uint32_t q = e < 2 ? raw[x].x : raw[x].y;
-      float y0 = __uint_as_float(q << 16) * up, y1 = __uint_as_float(q & 0xffff0000u) * up;
-      // what is not finite makes the row NaN (the conversion would saturate it)
-      if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
-      if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
-      const uint32_t q1 = e4m3x2(y0, y1);
-      const float2 g1 = from_e4m3x2(q1);
-      const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
-      b1 |= q1 << (8 * e);
-      b2 |= q2 << (8 * e);
+      for (int x = 0; x < N; ++x) raw[x] = load(w + (x0 + x) * W);
     }
-    const uint32_t off = swz((uint32_t)(r * DH + lane * E), DH);
-    if constexpr (E == 4) {
-      *reinterpret_cast<uint32_t*>(dst + off) = b1;
-      *reinterpret_cast<uint32_t*>(dst + kPart + off) = b2;
-    } else {
-      *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)b1;
-      *reinterpret_cast<uint16_t*>(dst + kPart + off) = (uint16_t)b2;
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      const int r = w + (x0 + x) * W;
+      uint32_t b1 = 0u, b2 = 0u;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t q = e < 2 ? raw[x].x : raw[x].y;
+        float y0 = __uint_as_float(q << 16) * up, y1 = __uint_as_float(q & 0xffff0000u) * up;
+        // what is not finite makes the row NaN (the conversion would saturate it)
+        if (odd) {
+          if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
+          if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
+        }
+        const uint32_t q1 = e4m3x2(y0, y1);
+        const float2 g1 = from_e4m3x2(q1);
+        const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
+        b1 |= q1 << (8 * e);
+        b2 |= q2 << (8 * e);
+      }
+      const uint32_t off = swz((uint32_t)(r * DH + lane * E), DH);
+      if constexpr (E == 4) {
+        *reinterpret_cast<uint32_t*>(dst + off) = b1;
+        *reinterpret_cast<uint32_t*>(dst + kPart + off) = b2;
+      } else {
+        *reinterpret_cast<uint16_t*>(dst + off) = (uint16_t)b1;
+        *reinterpret_cast<uint16_t*>(dst + kPart + off) = (uint16_t)b2;
+      }
     }
   }
   return __int_as_float((127 - sh) << 23);
 }
 
-// A node's row of V in shared memory (boxes of `row` bytes, `box` bytes apart): zeros in
-// place of elements that are not finite; whether there were any.
+// A slot's row of V in shared memory (boxes of `row` bytes, `box` bytes apart), behind the
+// sequence's nodes (`none`): zeros; of a node: zeros in place of elements that are not
+// finite.  Returns whether there were any.
 template <bool FP8>
-__device__ __noinline__ void zero_unfit(uint8_t* at, int row, int boxes, int box) {
+__device__ __forceinline__ bool clean_v_here(uint8_t* at, bool none, int row, int boxes, int box) {
+  // an exponent of all ones (an e4m3 of all ones) carries into the sign's place
+  constexpr uint32_t ones = FP8 ? 0x7f7f7f7fu : 0x7f807f80u;
+  constexpr uint32_t one = FP8 ? 0x01010101u : 0x00800080u;
+  constexpr uint32_t sign = FP8 ? 0x80808080u : 0x80008000u;
+  uint32_t hit = 0u;
 #pragma unroll 1
-  for (int x = 0; x < boxes; ++x)
-#pragma unroll 1
-    for (int q = 0; q < row / 4; ++q) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(at + x * box) + q;
-      uint32_t m = 0u;
-      if constexpr (FP8) {
-        for (int y = 0; y < 32; y += 8)
-          if (((*w >> y) & 0x7fu) == 0x7fu) m |= 0xffu << y;
+  for (int x = 0; x < boxes; ++x, at += box)
+#pragma unroll 4
+    for (int q = 0; q < row; q += 16) {
+      uint4* v = reinterpret_cast<uint4*>(at + q);
+      if (none) {
+        *v = make_uint4(0u, 0u, 0u, 0u);
       } else {
-        for (int y = 0; y < 32; y += 16)
-          if (((*w >> y) & 0x7f80u) == 0x7f80u) m |= 0xffffu << y;
+        uint4 w = *v;
+        const uint32_t m[4] = {((w.x & ones) + one) & sign, ((w.y & ones) + one) & sign,
+                               ((w.z & ones) + one) & sign, ((w.w & ones) + one) & sign};
+        if (m[0] | m[1] | m[2] | m[3]) {
+          hit = 1u;
+          // the sign's place to all of the element's
+          constexpr uint32_t width = FP8 ? 0xffu : 0xffffu;
+          constexpr int shift = FP8 ? 7 : 15;
+          w.x &= ~((m[0] >> shift) * width);
+          w.y &= ~((m[1] >> shift) * width);
+          w.z &= ~((m[2] >> shift) * width);
+          w.w &= ~((m[3] >> shift) * width);
+          *v = w;
+        }
       }
-      if (m) *w &= ~m;
     }
+  return hit != 0u;
+}
+
+// Which of a chunk's columns see each node of the sequence: vis[node] bit c, [kMaxNodes][2]
+// words, by the n threads of a group; `par` takes the sequence's parents.  A thread a node
+// of the chunk adds its columns to itself and its ancestors.
+__device__ __forceinline__ void build_seen_here(const TreeParams& p, int node0, int b, int nn,
+                                                int t, int n, int bar, int* par,
+                                                unsigned long long* vis) {
+  tc::named_bar_sync(bar, n);  // nobody reads the old ones any more
+  for (int k = t; k < nn; k += n) {
+    if (p.parent) par[k] = p.parent[(size_t)b * p.T + k];
+    vis[k] = 0ull;
+  }
+  tc::named_bar_sync(bar, n);
+  int node = node0 + t;
+  if (t < p.tn && node < nn) {
+    const unsigned long long cols = (~0ull >> (64 - p.gs)) << (t * p.gs);
+#pragma unroll 1
+    while (node >= 0) {
+      uint32_t* v = reinterpret_cast<uint32_t*>(vis + node);
+      if ((uint32_t)cols) atomicOr(v, (uint32_t)cols);
+      if (cols >> 32) atomicOr(v + 1, (uint32_t)(cols >> 32));
+      int up = p.parent ? par[node] : node - 1;
+      if (up < -1 || up >= node) {
+        set_status(p.status, FDLLM_ERR_BAD_INDEX);
+        up = -1;
+      }
+      node = up;
+    }
+  }
+  tc::named_bar_sync(bar, n);
+}
+
+// The two out of line in 8 bits (136 us for 141 of 32 rows over 64 sequences of 4096), in
+// line in 16 (a single token: 22.5 us for 24.4).
+template <bool FP8>
+__device__ __noinline__ bool clean_v_out(uint8_t* at, bool none, int row, int boxes, int box) {
+  return clean_v_here<FP8>(at, none, row, boxes, box);
+}
+template <bool FP8>
+__device__ __forceinline__ bool clean_v(uint8_t* at, bool none, int row, int boxes, int box) {
+  if constexpr (FP8)
+    return clean_v_out<FP8>(at, none, row, boxes, box);
+  else
+    return clean_v_here<FP8>(at, none, row, boxes, box);
+}
+__device__ __noinline__ void build_seen_out(const TreeParams& p, int node0, int b, int nn, int t,
+                                            int n, int bar, int* par, unsigned long long* vis) {
+  build_seen_here(p, node0, b, nn, t, n, bar, par, vis);
+}
+template <bool FP8>
+__device__ __forceinline__ void build_seen(const TreeParams& p, int node0, int b, int nn, int t,
+                                           int n, int bar, int* par, unsigned long long* vis) {
+  if constexpr (FP8)
+    build_seen_out(p, node0, b, nn, t, n, bar, par, vis);
+  else
+    build_seen_here(p, node0, b, nn, t, n, bar, par, vis);
+}
+
+// tc::mbar_wait with what follows a wait that is not over at once out of line
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return tc::mbar_wait(bar, parity, abort, status);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         int* status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  return wait_on(bar, parity, abort, status);
 }
 
 // orders this thread's view of memory, device-wide, around an atomic count
@@ -398,10 +506,24 @@ struct IdleClock {
   }
 };
 
+// Spins on a barrier's phase with the whole warp (a suspended wait wakes up late); false
+// after kWaitLimitNs.
+__device__ __noinline__ bool spin_on(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  IdleClock clk;
+  while (!__all_sync(kFull, tc::mbar_test(bar, parity)))
+    if (__any_sync(kFull, !clk.idle(abort, status))) return false;
+  return true;
+}
+__device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  if (__all_sync(kFull, tc::mbar_test(bar, parity))) return true;
+  return spin_on(bar, parity, abort, status);
+}
+
 // First unit of CTA c's range, and the CTA whose range holds unit u (the largest c
 // with lo(c) <= u; a double-precision estimate is put right with exact products).
 __device__ __forceinline__ int unit_lo(int total, int G, int c) {
-  return (int)((long long)total * c / G);
+  const long long a = (long long)total * c;
+  return a <= INT_MAX ? (int)a / G : (int)(a / G);
 }
 __device__ __forceinline__ int owner_of(int u, int total, int G) {
   const long long lim = ((long long)u + 1) * G;
@@ -471,6 +593,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   int* s_pre = reinterpret_cast<int*>(v_ring + NV * C::kTileBytes);
   int* s_len = s_pre + p.B + 1;
   int* s_nn = s_len + p.B;
+  // 8 bits, by V stage: the slots' K scales and V scales [2][128]
+  float* scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(s_pre) + Misc::seq_bytes(p.B));
   uint64_t* k_full = reinterpret_cast<uint64_t*>(misc + Misc::kBars);
   uint64_t* k_empty = k_full + 8;
   uint64_t* v_full = k_empty + 8;
@@ -490,12 +614,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   float* s_wred = reinterpret_cast<float*>(misc + Misc::kRed);
   float* seg_m = reinterpret_cast<float*>(misc + Misc::kSegM);
   float* seg_l = seg_m + 2 * 128;
-  uint8_t* col_node = misc + Misc::kCol;
-  int* col_off = reinterpret_cast<int*>(misc + Misc::kCol + 64);  // of a row in out
+  int* col_off = reinterpret_cast<int*>(misc + Misc::kCol);
   float* qsc = reinterpret_cast<float*>(misc + Misc::kQsc);  // [2], then the first split's maxima
   float* s_zero = reinterpret_cast<float*>(misc + Misc::kZero);  // [64] zeros
   int* s_par = reinterpret_cast<int*>(misc + Misc::kPar);
-  uint32_t* s_anc = reinterpret_cast<uint32_t*>(misc + Misc::kAnc);
+  unsigned long long* s_vis = reinterpret_cast<unsigned long long*>(misc + Misc::kVis);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -509,7 +632,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     for (int s = 0; s < 8; ++s) {
       tc::mbar_init(&k_full[s], 1);
       tc::mbar_init(&k_empty[s], 1);
-      tc::mbar_init(&v_full[s], 1);
+      tc::mbar_init(&v_full[s], FP8 ? 33 : 1);  // 8 bits: every lane's scales
       tc::mbar_init(&v_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -531,7 +654,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   if (tid < 64) {
     s_zero[tid] = 0.f;
     const int n = tid / p.gs;
-    col_node[tid] = (uint8_t)n;
     col_off[tid] = (n * p.Hq + tid - n * p.gs) * DH;
   }
   // rows of Q past the chunk's: zeros, whatever the product makes of them is not read
@@ -588,14 +710,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   const int u1 = cta < G ? unit_lo(U, G, cta + 1) : 0;
   const int T = u1 - u0;
 
+  // Where a chunk's first row is in q and out, and how many columns are rows of the sequence
+  // (with hs = 2 a chunk has one node).
+  auto row_of = [&](int qc, int b, int h) {
+    return (((size_t)b * p.T + qc / p.hs * p.tn) * p.Hq + h * p.g + qc % p.hs * p.gs) * DH;
+  };
+  auto columns = [&](int qc, int b) {
+    return min(p.tn, s_nn[b] - qc / p.hs * p.tn) * min(p.gs, p.g - qc % p.hs * p.gs);
+  };
+
   if (T == 0) {
     // no work for this CTA (it meets the others at the end)
   } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    // K and V each have their own ring, filled as soon as a stage frees; 16 bits: the one
+    // Q buffer takes the next item's rows as soon as the last QK of the running one is
+    // done.  8 bits: the slots' scales come with the V tiles, 4-byte copies by every lane
+    // (a head's scales start anywhere).
+    {
+      const bool leader = lane == 0;
       const uint64_t pol_kv = p.keep ? tc::policy_evict_normal() : tc::policy_evict_first();
       const uint64_t pol_q = tc::policy_evict_last();
-      int ik = 0, iv = 0, qn = 0;
+      int ik = 0, iv = 0, qn = 0, ks = 0, vs = 0;
+      uint32_t kph = 1u, vph = 1u;
       Cursor ck, cv, cq;
       ck.init(u0, S);
       cv = ck;
@@ -605,46 +742,66 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       while (iv < T || q_left > 0) {
         bool progressed = false;
         if constexpr (!FP8) {
-          if (q_left > 0 && tc::mbar_test(&q_empty[0], ((uint32_t)qn & 1u) ^ 1u)) {
-            const uint32_t bytes = (uint32_t)(p.tn * p.g) * 128u;
-            tc::mbar_arrive_expect_tx(&q_full[0], bytes * C::kBoxes);
+          if (q_left > 0 && __all_sync(kFull, tc::mbar_test(&q_empty[0], ((uint32_t)qn & 1u) ^ 1u))) {
+            if (leader) {
+              const uint32_t bytes = (uint32_t)(p.tn * p.g) * 128u;
+              tc::mbar_arrive_expect_tx(&q_full[0], bytes * C::kBoxes);
 #pragma unroll
-            for (int x = 0; x < C::kBoxes; ++x)
-              tc::tma_load_5d(q_buf + x * NQ * 128, &tm_q, &q_full[0], x * 64, 0, cq.h,
-                              cq.qc * p.tn, cq.b, pol_q);
+              for (int x = 0; x < C::kBoxes; ++x)
+                tc::tma_load_5d(q_buf + x * NQ * 128, &tm_q, &q_full[0], x * 64, 0, cq.h,
+                                cq.qc * p.tn, cq.b, pol_q);
+            }
             q_left -= cq.tb - cq.t;
             if (q_left > 0) cq.next_item(S);
             ++qn;
             progressed = true;
           }
         }
-        if (ik < T) {
-          const int ks = ik % NK;
-          if (tc::mbar_test(&k_empty[ks], ((uint32_t)(ik / NK) & 1u) ^ 1u)) {
+        if (ik < T && __all_sync(kFull, tc::mbar_test(&k_empty[ks], kph))) {
+          if (leader) {
             uint8_t* kd = k_ring + ks * C::kTileBytes;
             tc::mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x)
               tc::tma_load_3d(kd + x * C::kBoxBytes, &tm_k, &k_full[ks], x * 64, ck.t * kKT,
                               ck.b * p.Hkv + ck.h, pol_kv);
-            if (++ik < T) ck.next(S);
-            progressed = true;
           }
+          if (++ks == NK) {
+            ks = 0;
+            kph ^= 1u;
+          }
+          if (++ik < T) ck.next(S);
+          progressed = true;
         }
-        if (iv < ik) {
-          const int vs = iv % NV;
-          if (tc::mbar_test(&v_empty[vs], ((uint32_t)(iv / NV) & 1u) ^ 1u)) {
+        if (iv < ik && __all_sync(kFull, tc::mbar_test(&v_empty[vs], vph))) {
+          if (leader) {
             uint8_t* vd = v_ring + vs * C::kTileBytes;
             tc::mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x)
               tc::tma_load_3d(vd + x * C::kBoxBytes, &tm_v, &v_full[vs], x * 64, cv.t * kKT,
                               cv.b * p.Hkv + cv.h, pol_kv);
-            if (++iv < T) cv.next(S);
-            progressed = true;
           }
+          if constexpr (FP8) {
+            const size_t head = ((size_t)cv.b * p.Hkv + cv.h) * p.N;
+            float* dst = scales + vs * 256;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int slot = x * 32 + lane;
+              const size_t at = head + min(cv.t * kKT + slot, p.N - 1);
+              copy_async4(dst + slot, p.k_scale + at);
+              copy_async4(dst + 128 + slot, p.v_scale + at);
+            }
+            copy_async_arrive(&v_full[vs]);
+          }
+          if (++vs == NV) {
+            vs = 0;
+            vph ^= 1u;
+          }
+          if (++iv < T) cv.next(S);
+          progressed = true;
         }
-        if (!progressed && !clk.idle(abort_flag, p.status)) break;
+        if (!progressed && __any_sync(kFull, !clk.idle(abort_flag, p.status))) break;
         if (progressed) clk.reset();
       }
     }
@@ -656,7 +813,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // lane's own branch an MMA cost 77 cycles, more than the tensor cores take for it.)
     constexpr uint32_t swz_code = C::kBoxRow == 128 ? 2u : 4u;
     constexpr uint32_t p_swz = C::kPRow == 128 ? 2u : (C::kPRow == 64 ? 4u : 6u);
-    constexpr uint32_t full = 0xffffffffu;
+    constexpr uint32_t full = kFull;
     const bool leader = lane == 0;
     const uint32_t k_base = tc::smem_u32(k_ring), v_base = tc::smem_u32(v_ring);
     const uint32_t q_base = tc::smem_u32(q_buf), p_base = tc::smem_u32(p_buf);
@@ -800,29 +957,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     float* alpha = m_run + 64;
     float* alpha_o = alpha + 64;
     float* wred = s_wred + grp * 256;  // [4][64]
-    uint32_t* anc = s_anc + grp * 64 * kAncWords;
+    unsigned long long* vis = s_vis + grp * kMaxNodes;
     int* par = s_par + grp * kMaxNodes;
     float l[NQH];
     int e_ref = -1000;     // power of two that the segment's weights are taken against
-    int anc_key = -1;      // (chunk, sequence) whose ancestors are in shared memory
+    int vis_key = -1;      // (chunk, sequence) that vis stands for
     int pv_waited = -1;    // index of the last PV this thread waited for
     Cursor cs;
     cs.init(u0, S);
     const int item0 = u0 - cs.t;  // first unit of the item the range starts in
 
-    // Where the item's rows go in out, and how many columns are rows of the sequence.
-    auto out_of = [&](int qc, int b, int h) {
-      return p.out +
-             (((size_t)b * p.T + qc / p.hs * p.tn) * p.Hq + h * p.g + qc % p.hs * p.gs) * DH + kl;
-    };
-    auto columns = [&](int qc, int b) {  // (with hs = 2 a chunk has one node)
-      return min(p.tn, s_nn[b] - qc / p.hs * p.tn) * min(p.gs, p.g - qc % p.hs * p.gs);
-    };
     auto wait_pv = [&](int e) {
       if (e >= 0 && pv_waited < e) {
         // after a timeout every later wait returns at once: keep going, so that all
         // threads still meet at the same barriers
-        tc::mbar_wait(&pv_done[e & 1], (uint32_t)(e >> 1) & 1u, abort_flag, p.status);
+        wait_bar(&pv_done[e & 1], (uint32_t)(e >> 1) & 1u, abort_flag, p.status);
         pv_waited = e;
       }
     };
@@ -847,7 +996,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const int sl = d_seg & 1;
       const int* it = I->item[sl][grp];
       const int d_qc = it[0], d_b = it[1], d_h = it[2];
-      tc::mbar_wait(&seg_full[sl], (uint32_t)(d_seg >> 1) & 1u, abort_flag, p.status);
+      wait_bar(&seg_full[sl], (uint32_t)(d_seg >> 1) & 1u, abort_flag, p.status);
       tc::tc_fence_after();
       const float* sm = seg_m + sl * 128;  // [group][64]
       const float* ls = seg_l + sl * 128;
@@ -859,22 +1008,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const bool has = I->seg_has[sl][x] != 0;
         bad |= I->seg_bad[sl][x] != 0;
         const float unit = FP8 ? exp2f((float)(I->seg_e[sl][x] - C::kPOff)) : 1.f;
-        float y[NF];
+        float y[NF], z[C::kOParts > 1 ? 2 * NF : 1];
         const uint32_t at = tmem_o + (uint32_t)((sl * KG + x) * C::kOCols) + lane_off + (uint32_t)f0;
         tmem_ld_chunk(at, y, NF);
+        if constexpr (C::kOParts > 1) {
+          tmem_ld_chunk(at + NQ, z, NF);
+          tmem_ld_chunk(at + 2 * NQ, z + NF, NF);
+        }
         tc::tmem_wait_ld();
+        if constexpr (C::kOParts > 1) {
 #pragma unroll
-        for (int part = 1; part < C::kOParts; ++part) {
-          float z[NF];
-          tmem_ld_chunk(at + part * NQ, z, NF);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < NF; ++c) y[c] += z[c];
+          for (int c = 0; c < NF; ++c) y[c] += z[c] + z[NF + c];
         }
 #pragma unroll
         for (int c = 0; c < NF; ++c) {
           float w = unit;
-          if (KG == 2) w *= exp2f(sm[x * 64 + f0 + c] - fmaxf(sm[f0 + c], sm[64 + f0 + c]));
+          if (KG == 2) w *= ex2_approx(sm[x * 64 + f0 + c] - fmaxf(sm[f0 + c], sm[64 + f0 + c]));
           const float v = has ? y[c] * w : 0.f;
           o[c] = x == 0 ? v : o[c] + v;
         }
@@ -882,10 +1031,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       auto sums = [&](int c) {  // l of column c, both groups at the larger maximum
         if (KG == 1) return ls[c];
         const float M = fmaxf(sm[c], sm[64 + c]);
-        return exp2f(sm[c] - M) * ls[c] + exp2f(sm[64 + c] - M) * ls[64 + c];
+        return ex2_approx(sm[c] - M) * ls[c] + ex2_approx(sm[64 + c] - M) * ls[64 + c];
       };
       if (it[4]) {
-        __nv_bfloat16* o_at = out_of(d_qc, d_b, d_h);
+        __nv_bfloat16* o_at = p.out + row_of(d_qc, d_b, d_h) + kl;
         const int ncol = columns(d_qc, d_b);
         if (kl < DH) {
 #pragma unroll
@@ -919,24 +1068,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       d_fin = true;
     };
 
-    // 8 bits: the tile's slot scales, one tile ahead, by the thread that reads them.
-    // (Through shared memory: in registers they were spilled, which waits for the load.)
-    float2* scales = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(s_pre) + Misc::seq_bytes(p.B)) + st;
-    size_t sc_head = 0;  // the head's first scale
-    auto load_scales = [&](int t) {
-      const size_t i = sc_head + min(t * kKT + kl, p.N - 1);
-      copy_async4(&scales->x, p.k_scale + i);
-      copy_async4(&scales->y, p.v_scale + i);
-    };
-
     int i0 = 0;  // range index of the segment's first tile
+    int vst = grp;  // V stage of the group's next tile, and its phase
+    uint32_t vph = 0u;
     if constexpr (FP8) {
-      sc_head = ((size_t)cs.b * p.Hkv + cs.h) * p.N;
-      load_scales(cs.t + (KG == 2 ? grp : 0));
       // the range's first Q is split by all of these warps: nothing else is to do yet
       int* w_max = reinterpret_cast<int*>(qsc) + 2;
       const float unit = split_q<NQ, DH, C::kSmx / 32>(
-          p, cs.qc, cs.b, cs.h, s_nn[cs.b], warp - C::kFirst, q_buf, [&](uint32_t mx) {
+          static_cast<const __nv_bfloat16*>(p.q) + row_of(cs.qc, cs.b, cs.h), col_off,
+          columns(cs.qc, cs.b), warp - C::kFirst, q_buf, [&](uint32_t mx) {
+            tc::named_bar_sync(kBarAll, C::kSmx);  // a second call's writes come after the reads
             if (lane == 0) w_max[warp - C::kFirst] = (int)mx;
             tc::named_bar_sync(kBarAll, C::kSmx);
             return __reduce_max_sync(0xffffffffu, (uint32_t)w_max[lane & (C::kSmx / 32 - 1)]);
@@ -961,266 +1102,220 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       for (int i = KG == 2 ? i0 + ((i0 ^ grp) & 1) : i0;; i += KG) {
         const bool closing = i + KG >= i0 + nt;
         if (i < i0 + nt) {
-        const int t = cs.t + i - i0;
-        const bool tree = (t + 1) * kKT > len;  // the tile holds nodes (or slots past them)
-        if (tree && b * p.n_qc + qc != anc_key) {
-          // the chunk's nodes' ancestors, a thread a node
-          anc_key = b * p.n_qc + qc;
-          tc::named_bar_sync(bar_a, GT);  // nobody reads the old ones any more
-          if (p.parent)
-            for (int n = gt; n < s_nn[b]; n += GT) par[n] = p.parent[(size_t)b * p.T + n];
-          for (int w = gt; w < p.tn * kAncWords; w += GT) anc[w] = 0u;
-          tc::named_bar_sync(bar_a, GT);
-          int n = qc / p.hs * p.tn + gt;
-          if (gt < p.tn && n < s_nn[b]) {
-            uint32_t* a = anc + gt * kAncWords;
-            if (p.parent) {
-#pragma unroll 1
-              while (n >= 0) {
-                a[n >> 5] |= 1u << (n & 31);
-                int up = par[n];
-                if (up < -1 || up >= n) {
-                  set_status(p.status, FDLLM_ERR_BAD_INDEX);
-                  up = -1;
-                }
-                n = up;
-              }
-            } else {
-#pragma unroll 1
-              for (int w = 0; w <= n >> 5; ++w)
-                a[w] = w < (n >> 5) ? ~0u : ~0u >> (31 - (n & 31));
-            }
+          const int t = cs.t + i - i0;
+          const bool tree = (t + 1) * kKT > len;  // the tile holds nodes (or slots past them)
+          if (tree && b * p.n_qc + qc != vis_key) {
+            vis_key = b * p.n_qc + qc;
+            build_seen<FP8>(p, qc / p.hs * p.tn, b, s_nn[b], gt, GT, bar_a, par, vis);
           }
-          tc::named_bar_sync(bar_a, GT);
-        }
-        float ksc = p.qk_scale, vs = 1.f;
-        if constexpr (FP8) {
-          copy_async_wait();
-          const float2 f = *scales;
-          ksc *= f.x * qsc[seg & 1];
-          vs = f.y;
-          if (i + KG < i0 + nt) load_scales(t + KG);
-        }
-        const int slot = t * kKT + kl;
-        const bool zero_v = tree && slot >= lim;  // this slot's V goes into no sum
+          const int slot = t * kKT + kl;
+          const bool zero_v = tree && slot >= lim;  // this slot's V goes into no sum
+          uint32_t seen = ~0u;                      // columns that see the slot
+          if (tree && slot >= len)
+            seen = slot < lim ? (uint32_t)(vis[slot - len] >> c0) : 0u;
 
-        const int sb = i & 1;
-        tc::mbar_wait(&s_full[sb], (uint32_t)(i >> 1) & 1u, abort_flag, p.status);
-        tc::tc_fence_after();
-
-        // ---- scores (log2 units) against the running maximum: row kl of S^T, this
-        // thread's columns.  The maximum is raised when a score exceeds it by more than
-        // 2^kThresh (masked scores never do); a segment's first tile sets it.  Then the
-        // scores are formed again, as they are for their maxima (pass 1) and against the
-        // new maximum (pass 2): one copy of the code, S being there until the end.
-        float d[NQH];  // exponents of the weights
-        int pass = first ? 1 : 0;
-        bool any = first;
-#pragma unroll 1
-        for (;;) {
-          const uint32_t at = tmem + lane_off + sb * C::kSCols + c0;
-#pragma unroll
-          for (int c = 0; c < NQH; c += 16) tmem_ld_chunk(at + c, d + c, 16);
+          const int sb = i & 1;
+          wait_bar(&s_full[sb], (uint32_t)(i >> 1) & 1u, abort_flag, p.status);
+          tc::tc_fence_after();
+          float ksc = p.qk_scale, vs = 1.f;
           if constexpr (FP8) {
-            float d2[NQH];
-#pragma unroll
-            for (int c = 0; c < NQH; c += 16) tmem_ld_chunk(at + NQ + c, d2 + c, 16);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < NQH; ++c) d[c] += d2[c];
-          } else {
-            tc::tmem_wait_ld();
+            wait_bar(&v_full[vst], vph, abort_flag, p.status);
+            const float* sc = scales + vst * 256 + kl;
+            ksc *= sc[0] * qsc[seg & 1];
+            vs = sc[128];
           }
-          const float4* m4 = reinterpret_cast<const float4*>((pass == 1 ? s_zero : m_run) + c0);
+
+          // ---- scores (log2 units) against the running maximum: row kl of S^T, this
+          // thread's columns.  The maximum is raised when a score exceeds it by more than
+          // 2^kThresh (masked scores never do); a segment's first tile sets it.  For that the
+          // scores are formed again as they are (pass 1): one copy of the code, S being there
+          // until the end.
+          float d[NQH];  // exponents of the weights
+          int pass = first ? 1 : 0;
+          bool any = first;
+#pragma unroll 1
+          for (;;) {
+            const uint32_t at = tmem + lane_off + sb * C::kSCols + c0;
 #pragma unroll
-          for (int c = 0; c < NQH; c += 4) {
-            const float4 m = m4[c / 4];
-            d[c] = fmaf(d[c], ksc, -m.x);
-            d[c + 1] = fmaf(d[c + 1], ksc, -m.y);
-            d[c + 2] = fmaf(d[c + 2], ksc, -m.z);
-            d[c + 3] = fmaf(d[c + 3], ksc, -m.w);
-          }
-          if (tree) {
-            const int j = slot - len;
-            if (slot >= lim) {
+            for (int c = 0; c < NQH; c += 16) tmem_ld_chunk(at + c, d + c, 16);
+            if constexpr (FP8) {
+              float d2[NQH];
 #pragma unroll
-              for (int c = 0; c < NQH; ++c) d[c] = -INFINITY;
-            } else if (j >= 0) {
-              const uint32_t* aw = anc + (j >> 5);
+              for (int c = 0; c < NQH; c += 16) tmem_ld_chunk(at + NQ + c, d2 + c, 16);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < NQH; ++c) d[c] += d2[c];
+            } else {
+              tc::tmem_wait_ld();
+            }
+            const float4* m4 = reinterpret_cast<const float4*>((pass == 1 ? s_zero : m_run) + c0);
+#pragma unroll
+            for (int c = 0; c < NQH; c += 4) {
+              const float4 m = m4[c / 4];
+              d[c] = fmaf(d[c], ksc, -m.x);
+              d[c + 1] = fmaf(d[c + 1], ksc, -m.y);
+              d[c + 2] = fmaf(d[c + 2], ksc, -m.z);
+              d[c + 3] = fmaf(d[c + 3], ksc, -m.w);
+            }
+            if (tree) {
 #pragma unroll
               for (int c = 0; c < NQH; ++c)
-                if (!((aw[(int)col_node[c0 + c] * kAncWords] >> (j & 31)) & 1u)) d[c] = -INFINITY;
+                if (!((seen >> c) & 1u)) d[c] = -INFINITY;
             }
-          }
-          if (pass == 2) break;
-          int vexp = -1000;
-          if constexpr (FP8) {
-            // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1), at least
-            // 2^-100; scales of slots that go into no sum, zero ones and those that are
-            // not finite do not count
-            const int eb = (__float_as_int(vs) >> 23) & 255;
-            if (!zero_v && eb > 0 && eb < 255) vexp = max(eb - 127, -100);
-          }
-          if (pass == 0) {
-            float top = d[0];
+            int vexp = -1000;
+            if constexpr (FP8) {
+              // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1), at least
+              // 2^-100; scales of slots that go into no sum, zero ones and those that are
+              // not finite do not count
+              const int eb = (__float_as_int(vs) >> 23) & 255;
+              if (!zero_v && eb > 0 && eb < 255) vexp = max(eb - 127, -100);
+            }
+            if (pass == 0) {
+              float top = d[0];
 #pragma unroll
-            for (int c = 1; c < NQH; ++c) top = fmaxf(top, d[c]);
-            any = bar_any(bar_b, GT, top > C::kThresh || (FP8 && vexp > e_ref));
-            if (!any) break;
-            pass = 1;
-            continue;
-          }
+              for (int c = 1; c < NQH; ++c) top = fmaxf(top, d[c]);
+              any = bar_any(bar_b, GT, top > C::kThresh || (FP8 && vexp > e_ref));
+              if (!any) break;
+              pass = 1;
+              continue;
+            }
 #pragma unroll
-          for (int c = 0; c < NQH; ++c) {
-            const float wm = warp_max(d[c]);
-            if (lane == c) wred[quarter * 64 + c0 + c] = wm;
-          }
-          if constexpr (FP8) {
-            const int e = __reduce_max_sync(0xffffffffu, vexp);
-            if (lane == 0 && c0 == 0) I->vexp[grp][quarter] = e;
-          }
-          tc::named_bar_sync(bar_a, GT);
-          float e_scale = 1.f;
-          if constexpr (FP8) {
-            int e_new = e_ref;
+            for (int c = 0; c < NQH; ++c) {
+              const float wm = warp_max(d[c]);
+              if (lane == c) wred[quarter * 64 + c0 + c] = wm;
+            }
+            if constexpr (FP8) {
+              const int e = __reduce_max_sync(0xffffffffu, vexp);
+              if (lane == 0 && c0 == 0) I->vexp[grp][quarter] = e;
+            }
+            tc::named_bar_sync(bar_a, GT);
+            float e_scale = 1.f;
+            if constexpr (FP8) {
+              int e_new = e_ref;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) e_new = max(e_new, I->vexp[grp][w]);
-            // 2^(e_ref - e_new): 0 from the start value
-            e_scale = e_ref - e_new < -126 ? 0.f : __int_as_float((e_ref - e_new + 127) << 23);
-            e_ref = e_new;
-          }
-          if (gt < NQ) {
-            const float mo = first ? kNone : m_run[gt];
-            const float tm = fmaxf(fmaxf(wred[gt], wred[64 + gt]), fmaxf(wred[128 + gt], wred[192 + gt]));
-            const float mn = (tm - mo > C::kThresh) ? tm : mo;
-            const float al = exp2f(mo - mn);
-            alpha[gt] = al;
-            alpha_o[gt] = al * e_scale;
-            m_run[gt] = mn;
-          }
-          tc::named_bar_sync(bar_a, GT);
+              for (int w = 0; w < 4; ++w) e_new = max(e_new, I->vexp[grp][w]);
+              // 2^(e_ref - e_new): 0 from the start value
+              e_scale = e_ref - e_new < -126 ? 0.f : __int_as_float((e_ref - e_new + 127) << 23);
+              e_ref = e_new;
+            }
+            if (gt < NQ) {
+              const float mo = first ? kNone : m_run[gt];
+              const float tm = fmaxf(fmaxf(wred[gt], wred[64 + gt]), fmaxf(wred[128 + gt], wred[192 + gt]));
+              const float mn = (tm - mo > C::kThresh) ? tm : mo;
+              const float al = ex2_approx(mo - mn);
+              alpha[gt] = al;
+              alpha_o[gt] = al * e_scale;
+              m_run[gt] = mn;
+            }
+            tc::named_bar_sync(bar_a, GT);
 #pragma unroll
-          for (int c = 0; c < NQH; ++c) l[c] *= alpha[c0 + c];
-          pass = 2;
-        }
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s_empty[sb]);
+            for (int c = 0; c < NQH; ++c) {
+              l[c] *= alpha[c0 + c];
+              d[c] -= m_run[c0 + c];
+            }
+            break;
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s_empty[sb]);
 
-        // ---- P buffer i&1 is free once PV(i-2) is done; rescaling O needs the group's
-        // last PV
-        wait_pv(i - 2);
-        if (any && !first) {
-          if (KG == 1) wait_pv(i - 1);
-          tc::tc_fence_after();
-          const uint32_t at =
-              tmem_o + (uint32_t)(((seg & 1) * KG + grp) * C::kOCols) + lane_off + (uint32_t)c0;
-          float o[8];
+          // ---- P buffer i&1 is free once PV(i-2) is done; rescaling O needs the group's
+          // last PV
+          wait_pv(i - 2);
+          if (any && !first) {
+            if (KG == 1) wait_pv(i - 1);
+            tc::tc_fence_after();
+            const uint32_t at =
+                tmem_o + (uint32_t)(((seg & 1) * KG + grp) * C::kOCols) + lane_off + (uint32_t)c0;
+            float o[8];
 #pragma unroll 1
-          for (int cc = 0; cc < C::kOParts * NQH; cc += 8) {
-            const int c1 = cc & (NQH - 1), part = cc / NQH;
-            tc::tmem_ld8(at + part * NQ + c1, o);
-            tc::tmem_wait_ld();
+            for (int cc = 0; cc < C::kOParts * NQH; cc += 8) {
+              const int c1 = cc & (NQH - 1), part = cc / NQH;
+              tc::tmem_ld8(at + part * NQ + c1, o);
+              tc::tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 8; ++c) o[c] *= alpha_o[c0 + c1 + c];
-            tc::tmem_st8(at + part * NQ + c1, o);
-          }
-          tc::tmem_wait_st();
-        }
-        if (tree && slot >= len && c0 == 0) {
-          // V of a slot past the nodes: zeros; of a node: zeros in place of what is not
-          // finite
-          tc::mbar_wait(&v_full[i % NV], (uint32_t)(i / NV) & 1u, abort_flag, p.status);
-          uint8_t* row = v_ring + (i % NV) * C::kTileBytes + kl * C::kBoxRow;
-          if (zero_v) {
-#pragma unroll 2
-            for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
-              const int x = q / (C::kBoxRow / 16);
-              *reinterpret_cast<uint4*>(row + x * C::kBoxBytes + (q - x * (C::kBoxRow / 16)) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < 8; ++c) o[c] *= alpha_o[c0 + c1 + c];
+              tc::tmem_st8(at + part * NQ + c1, o);
             }
-          } else {
-            // an exponent of all ones (an e4m3 of all ones) carries into the sign's place
-            constexpr uint32_t ones = FP8 ? 0x7f7f7f7fu : 0x7f807f80u;
-            constexpr uint32_t one = FP8 ? 0x01010101u : 0x00800080u;
-            constexpr uint32_t sign = FP8 ? 0x80808080u : 0x80008000u;
-            uint32_t hit = 0u;
-#pragma unroll 4
-            for (int q = 0; q < (int)(C::kBoxes * C::kBoxRow / 16); ++q) {
-              const int x = q / (C::kBoxRow / 16);
-              const uint4 w = *reinterpret_cast<const uint4*>(row + x * C::kBoxBytes +
-                                                              (q - x * (C::kBoxRow / 16)) * 16);
-              hit |= ((w.x & ones) + one) | ((w.y & ones) + one) | ((w.z & ones) + one) |
-                     ((w.w & ones) + one);
-            }
-            if ((hit & sign) != 0u) zero_unfit<FP8>(row, C::kBoxRow, C::kBoxes, C::kBoxBytes);
-            if ((hit & sign) != 0u || (FP8 && not_finite(vs))) I->bad_run[grp] = 1;
+            tc::tmem_wait_st();
           }
-        }
+          if (tree && slot >= len && c0 == 0) {
+            // V of a slot past the nodes: zeros; of a node: zeros in place of what is not
+            // finite
+            wait_bar(&v_full[vst], vph, abort_flag, p.status);
+            if (clean_v<FP8>(v_ring + vst * C::kTileBytes + kl * C::kBoxRow, zero_v, C::kBoxRow,
+                             C::kBoxes, C::kBoxBytes) ||
+                (FP8 && !zero_v && not_finite(vs)))
+              I->bad_run[grp] = 1;
+          }
 
-        // ---- P = 2^(s - m) into row kl of the MN-major swizzled P^T tile
-        uint8_t* pb = p_buf + (i & 1) * C::kPBuf;
-        if constexpr (FP8) {
-          // the weight carries the slot's scale against 2^e_ref, times 2^kPOff
-          float w = 0.f;
-          if (!zero_v && !(tree && slot >= len && not_finite(vs)))
-            w = vs * __int_as_float((127 + min(C::kPOff - e_ref, 127)) << 23);
-          uint32_t pk[3][NQH / 4];
+          // ---- P = 2^(s - m) into row kl of the MN-major swizzled P^T tile
+          uint8_t* pb = p_buf + (i & 1) * C::kPBuf;
+          if constexpr (FP8) {
+            // the weight carries the slot's scale against 2^e_ref, times 2^kPOff
+            float w = 0.f;
+            if (!zero_v && !(tree && slot >= len && not_finite(vs)))
+              w = vs * __int_as_float((127 + min(C::kPOff - e_ref, 127)) << 23);
+            uint32_t pk[3][NQH / 4];
 #pragma unroll
-          for (int c = 0; c < NQH; c += 4) {
-            uint32_t hp[2][3];
+            for (int c = 0; c < NQH; c += 4) {
+              uint32_t hp[2][3];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float p0 = ex2_approx(d[c + 2 * y]);
-              const float p1 = ex2_approx(d[c + 2 * y + 1]);
-              l[c + 2 * y] += p0;
-              l[c + 2 * y + 1] += p1;
-              // fp16 value h; its upper byte is e5m2, cut off: h = hi + rest, twice; the
-              // last part is rounded (half a unit added below the byte; it never carries
-              // past 16 bits, parts being far below the largest)
-              const uint32_t h = pack_f16x2(p0 * w, p1 * w);
-              const uint32_t h1 = h & 0xff00ff00u;
-              const uint32_t r1 = sub_f16x2(h, h1);
-              const uint32_t h2 = r1 & 0xff00ff00u;
-              const uint32_t r2 = sub_f16x2(r1, h2);
-              hp[y][0] = h1;
-              hp[y][1] = h2;
-              hp[y][2] = r2 + 0x00800080u;
+              for (int y = 0; y < 2; ++y) {
+                const float p0 = ex2_approx(d[c + 2 * y]);
+                const float p1 = ex2_approx(d[c + 2 * y + 1]);
+                l[c + 2 * y] += p0;
+                l[c + 2 * y + 1] += p1;
+                // fp16 value h; its upper byte is e5m2, cut off: h = hi + rest, twice; the
+                // last part is rounded (half a unit added below the byte; it never carries
+                // past 16 bits, parts being far below the largest)
+                const uint32_t h = pack_f16x2(p0 * w, p1 * w);
+                const uint32_t h1 = h & 0xff00ff00u;
+                const uint32_t r1 = sub_f16x2(h, h1);
+                const uint32_t h2 = r1 & 0xff00ff00u;
+                const uint32_t r2 = sub_f16x2(r1, h2);
+                hp[y][0] = h1;
+                hp[y][1] = h2;
+                hp[y][2] = r2 + 0x00800080u;
+              }
+#pragma unroll
+              for (int part = 0; part < 3; ++part)
+                pk[part][c / 4] = __byte_perm(hp[0][part], hp[1][part], 0x7531);
             }
 #pragma unroll
             for (int part = 0; part < 3; ++part)
-              pk[part][c / 4] = __byte_perm(hp[0][part], hp[1][part], 0x7531);
+#pragma unroll
+              for (int ch = 0; ch < NQH / 16; ++ch)
+                *reinterpret_cast<uint4*>(
+                    pb + swz((uint32_t)(kl * C::kPRow + part * NQ + c0 + ch * 16), C::kPRow)) =
+                    make_uint4(pk[part][4 * ch], pk[part][4 * ch + 1], pk[part][4 * ch + 2],
+                               pk[part][4 * ch + 3]);
+          } else {
+            uint32_t pk[NQH / 2];
+#pragma unroll
+            for (int c = 0; c < NQH; c += 2) {
+              const float p0 = ex2_approx(d[c]);
+              const float p1 = ex2_approx(d[c + 1]);
+              l[c] += p0;
+              l[c + 1] += p1;
+              pk[c / 2] = pack_bf16x2(p0, p1);
+            }
+#pragma unroll
+            for (int ch = 0; ch < NQH / 8; ++ch)
+              *reinterpret_cast<uint4*>(pb + swz((uint32_t)(kl * C::kPRow + c0 * 2 + ch * 16), C::kPRow)) =
+                  make_uint4(pk[ch * 4], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
           }
-#pragma unroll
-          for (int part = 0; part < 3; ++part)
-#pragma unroll
-            for (int ch = 0; ch < NQH / 16; ++ch)
-              *reinterpret_cast<uint4*>(
-                  pb + swz((uint32_t)(kl * C::kPRow + part * NQ + c0 + ch * 16), C::kPRow)) =
-                  make_uint4(pk[part][4 * ch], pk[part][4 * ch + 1], pk[part][4 * ch + 2],
-                             pk[part][4 * ch + 3]);
-        } else {
-          uint32_t pk[NQH / 2];
-#pragma unroll
-          for (int c = 0; c < NQH; c += 2) {
-            const float p0 = ex2_approx(d[c]);
-            const float p1 = ex2_approx(d[c + 1]);
-            l[c] += p0;
-            l[c + 1] += p1;
-            pk[c / 2] = pack_bf16x2(p0, p1);
+          tc::fence_proxy_async_smem();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&p_full[i & 1]);
+          first = false;
+          last = i;
+          vst += KG;
+          if (vst >= NV) {
+            vst -= NV;
+            vph ^= 1u;
           }
-#pragma unroll
-          for (int ch = 0; ch < NQH / 8; ++ch)
-            *reinterpret_cast<uint4*>(pb + swz((uint32_t)(kl * C::kPRow + c0 * 2 + ch * 16), C::kPRow)) =
-                make_uint4(pk[ch * 4], pk[ch * 4 + 1], pk[ch * 4 + 2], pk[ch * 4 + 3]);
-        }
-        tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&p_full[i & 1]);
-        first = false;
-        last = i;
-
         }
 
         // ---- the segment before: final once its last PV is two tiles back, written a
@@ -1238,13 +1333,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
       // ---- close the segment
       if (last >= 0) {
+        // l summed over the warp's slots: each round gives half of the columns away, so that
+        // a pair of lanes ends with one column's sum
+        static_assert(NQH == 16, "16 columns a thread");
 #pragma unroll
-        for (int c = 0; c < NQH; ++c) {
-          float v = l[c];
+        for (int o = 16, w = 8; w >= 1; o >>= 1, w >>= 1) {
+          const bool up = lane & o;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == c) wred[quarter * 64 + c0 + c] = v;
+          for (int c = 0; c < w; ++c) {
+            const float mine = up ? l[c + w] : l[c], gone = up ? l[c] : l[c + w];
+            l[c] = mine + __shfl_xor_sync(0xffffffffu, gone, o);
+          }
         }
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+        if (!(lane & 1)) wred[quarter * 64 + c0 + (lane >> 1)] = l[0];
         tc::named_bar_sync(bar_a, GT);
       }
       const int sl = seg & 1;
@@ -1275,10 +1377,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       i0 += nt;
       if (i0 < T) {
         cs.next_item(S);
-        if constexpr (FP8) {
-          sc_head = ((size_t)cs.b * p.Hkv + cs.h) * p.N;
-          load_scales(KG == 2 ? (i0 ^ grp) & 1 : 0);
-        }
       }
     }
 
@@ -1305,7 +1403,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         return p.partials + ((size_t)cb * 2 + sl) * C::kPartFloats;
       };
       constexpr int kJ = 3;  // contributors of a round
-      __nv_bfloat16* o_at = out_of(at.qc, at.b, at.h);
+      __nv_bfloat16* o_at = p.out + row_of(at.qc, at.b, at.h) + kl;
       const int ncol = columns(at.qc, at.b);
       const int d_row = kl < DH ? kl : 0;
       float bad = 0.f;
@@ -1365,27 +1463,27 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
   } else {
     // ------------------------------------------------------------ Q, finisher
-    // 8 bits: the next items' rows as two e4m3 parts, each into the Q buffer its QKs will
-    // read (the range's first is split by the softmax warps), by warps 2 and 3.  Then
-    // warp 2, for each partial of this CTA: wait until the softmax warps have issued its
-    // stores, make them visible device-wide, count this contributor in.  The last of an
-    // item's contributors merges it, after its range.
+    // 8 bits: the next items' rows as two e4m3 parts, each in the Q buffer its QKs will read
+    // (the range's first is split by the softmax warps).  Then, for each partial of this
+    // CTA: wait until the softmax warps have issued its stores, make them visible
+    // device-wide, count this contributor in.  The last of an item's contributors merges
+    // it, after its range.
     if constexpr (FP8) {
-      int* w_max = reinterpret_cast<int*>(qsc) + 18;  // [2 buffers][2 warps]
+      int* w_max = reinterpret_cast<int*>(qsc) + 18;  // [2]
       Cursor cq;
       cq.init(u0, S);
       int left = T - (cq.tb - cq.t);
       for (int n = 1; left > 0; ++n) {
         const int qb = n & 1;
         cq.next_item(S);
-        tc::mbar_wait(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status);
+        wait_bar(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status);
         const float unit = split_q<NQ, DH, 2>(
-            p, cq.qc, cq.b, cq.h, s_nn[cq.b], warp - 2, q_buf + qb * C::kQParts * C::kQPart,
-            [&](uint32_t mx) {
-              // (read by both before either can write this buffer's again: two rounds on)
-              if (lane == 0) w_max[2 * qb + warp - 2] = (int)mx;
+            static_cast<const __nv_bfloat16*>(p.q) + row_of(cq.qc, cq.b, cq.h), col_off,
+            columns(cq.qc, cq.b), warp - 2, q_buf + qb * C::kQParts * C::kQPart, [&](uint32_t mx) {
+              tc::named_bar_sync(7, 64);  // the last call's are read
+              if (lane == 0) w_max[warp - 2] = (int)mx;
               tc::named_bar_sync(7, 64);
-              return (uint32_t)max(w_max[2 * qb], w_max[2 * qb + 1]);
+              return (uint32_t)max(w_max[0], w_max[1]);
             });
         if (warp == 2 && lane == 0) qsc[qb] = unit;
         tc::fence_proxy_async_smem();
@@ -1395,38 +1493,38 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       }
     }
     if (warp == C::kFinisher) {
-    if (lane == 0) {
-      I->merge_u[0] = -1;
-      I->merge_u[1] = -1;
-      Cursor ca, cz;
-      ca.init(u0, S);
-      cz.init(u1 - 1, S);
-      for (int slot = 0; slot < 2; ++slot) {
-        const int iu = slot == 0 ? u0 - ca.t : u1 - 1 - cz.t;
-        const int tb = slot == 0 ? ca.tb : cz.tb;
-        if (slot == 1 && iu == u0 - ca.t) break;
-        if (u0 <= iu && u1 >= iu + tb) continue;  // whole: the softmax warps write it
-        bool ready = false;
-        IdleClock clk;
-        while (!(ready = tc::mbar_test(&fin_full[slot], 0u))) {
-          __nanosleep(64);
-          if (!clk.idle(abort_flag, p.status)) break;
-        }
-        if (!ready) break;
-        fence_gpu();
-        const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + tb - 1, U, G);
-        // an item that goes on behind CTA c_first's range is the only one to do so, so
-        // c_first names its counter
-        const unsigned prev = atomicAdd(&p.cnt[c_first], 1u);
-        if (prev == (unsigned)(c_last - c_first)) {
+      if (lane == 0) {
+        I->merge_u[0] = -1;
+        I->merge_u[1] = -1;
+        Cursor ca, cz;
+        ca.init(u0, S);
+        cz.init(u1 - 1, S);
+        for (int slot = 0; slot < 2; ++slot) {
+          const int iu = slot == 0 ? u0 - ca.t : u1 - 1 - cz.t;
+          const int tb = slot == 0 ? ca.tb : cz.tb;
+          if (slot == 1 && iu == u0 - ca.t) break;
+          if (u0 <= iu && u1 >= iu + tb) continue;  // whole: the softmax warps write it
+          bool ready = false;
+          IdleClock clk;
+          while (!(ready = tc::mbar_test(&fin_full[slot], 0u))) {
+            __nanosleep(64);
+            if (!clk.idle(abort_flag, p.status)) break;
+          }
+          if (!ready) break;
           fence_gpu();
-          p.cnt[c_first] = 0u;  // for the next call
-          I->merge_u[slot] = iu;
+          const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + tb - 1, U, G);
+          // an item that goes on behind CTA c_first's range is the only one to do so, so
+          // c_first names its counter
+          const unsigned prev = atomicAdd(&p.cnt[c_first], 1u);
+          if (prev == (unsigned)(c_last - c_first)) {
+            fence_gpu();
+            p.cnt[c_first] = 0u;  // for the next call
+            I->merge_u[slot] = iu;
+          }
         }
       }
-    }
-    __syncwarp();
-    tc::named_bar_sync(5, kSmx + 32);
+      __syncwarp();
+      tc::named_bar_sync(5, kSmx + 32);
     }
   }
 
@@ -1468,7 +1566,7 @@ TreePlan plan(const TreeAttnArgs& a, int num_sms) {
   qbytes = align_up(qbytes, 1024);
   const size_t pbytes = 2 * kKT * (a.fp8 ? 128 : nqp * 2);
   const size_t misc = Misc::kBytes + Misc::seq_bytes(a.B) +
-                      (a.fp8 ? Cfg<32, 128, true>::kSmx * sizeof(float2) : 0);
+                      (a.fp8 ? 8 * 1024 : 0);  // 8 stages of scales
   const size_t fixed = 1024 + qbytes + pbytes + misc;
   int tiles = (int)((kSmemBudget - fixed) / tile);
   if (tiles > 16) tiles = 16;
