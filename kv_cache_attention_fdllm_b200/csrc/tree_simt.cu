@@ -1,4 +1,4 @@
-// Attention of a tree of drafted tokens over a cache, on the CUDA cores.
+// Attention of a tree of drafted tokens over an fp32 cache, on the CUDA cores.
 //
 // out = softmax(q K^T / sqrt(dh)) V over the slots in front of the tree, a node's
 // ancestors and itself; query heads share kv heads in groups of g = Hq / Hkv.
@@ -21,22 +21,9 @@ constexpr int kNW = 8;
 constexpr int kWords = FDLLM_MAX_TREE_NODES / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float e4m3_to_float(uint8_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
-  float f;
-  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(h));
-  return f;
-}
-__device__ __forceinline__ float ld_elt(const float* p) { return *p; }
-__device__ __forceinline__ float ld_elt(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float ld_elt(const uint8_t* p) { return e4m3_to_float(*p); }
-
-// T: q and out, C: the cache (uint8_t: e4m3 with scales)
-template <typename T, typename C, int EPL>
+template <int EPL>
 __global__ void __launch_bounds__(kNW * 32) tree_simt(TreeAttnArgs a) {
   constexpr int dh = EPL * 32;
-  constexpr bool kFp8 = sizeof(C) == 1;
   __shared__ float sm_m[kNW][kQG], sm_l[kNW][kQG];
   __shared__ float sm_acc[kNW][kQG][dh];
   __shared__ uint32_t anc[kQG][kWords];  // ancestors of each row's node, and itself
@@ -78,9 +65,9 @@ __global__ void __launch_bounds__(kNW * 32) tree_simt(TreeAttnArgs a) {
     used[i] = t < nn;
 #pragma unroll
     for (int e = 0; e < EPL; ++e)
-      q[i][e] = used[i] ? qscale * ld_elt(static_cast<const T*>(a.q) +
-                                          (((size_t)b * a.T + t) * a.Hq + h * g + j) * dh +
-                                          lane * EPL + e)
+      q[i][e] = used[i] ? qscale * static_cast<const float*>(
+                                       a.q)[(((size_t)b * a.T + t) * a.Hq + h * g + j) * dh +
+                                            lane * EPL + e]
                         : 0.f;
   }
   float m[kQG], l[kQG], acc[kQG][EPL];
@@ -92,8 +79,8 @@ __global__ void __launch_bounds__(kNW * 32) tree_simt(TreeAttnArgs a) {
     for (int e = 0; e < EPL; ++e) acc[i][e] = 0.f;
   }
   const size_t head = ((size_t)b * a.Hkv + h) * a.N;
-  const C* K = static_cast<const C*>(a.k_cache) + head * dh + lane * EPL;
-  const C* V = static_cast<const C*>(a.v_cache) + head * dh + lane * EPL;
+  const float* K = static_cast<const float*>(a.k_cache) + head * dh + lane * EPL;
+  const float* V = static_cast<const float*>(a.v_cache) + head * dh + lane * EPL;
   for (int s = warp; s < len + nn; s += kNW) {
     bool see[kQG];
     bool any = false;
@@ -107,16 +94,8 @@ __global__ void __launch_bounds__(kNW * 32) tree_simt(TreeAttnArgs a) {
     float k[EPL], v[EPL];
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
-      k[e] = ld_elt(K + (size_t)s * dh + e);
-      v[e] = ld_elt(V + (size_t)s * dh + e);
-    }
-    if constexpr (kFp8) {
-      const float ks = a.k_scale[head + s], vs = a.v_scale[head + s];
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) {
-        k[e] *= ks;
-        v[e] *= vs;
-      }
+      k[e] = K[(size_t)s * dh + e];
+      v[e] = V[(size_t)s * dh + e];
     }
 #pragma unroll
     for (int i = 0; i < kQG; ++i) {
@@ -128,7 +107,7 @@ __global__ void __launch_bounds__(kNW * 32) tree_simt(TreeAttnArgs a) {
       if (!see[i]) continue;
       const float mn = fmaxf(m[i], x);
       const float sc = (m[i] == -INFINITY) ? 0.f : exp2f(m[i] - mn);
-      const float p = exp2f(x - mn);
+      const float p = x == -INFINITY ? 0.f : exp2f(x - mn);  // not 2^(-inf + inf)
       l[i] = l[i] * sc + p;
 #pragma unroll
       for (int e = 0; e < EPL; ++e) acc[i][e] = fmaf(p, v[e], acc[i][e] * sc);
@@ -157,30 +136,19 @@ __global__ void __launch_bounds__(kNW * 32) tree_simt(TreeAttnArgs a) {
       num += sm_acc[w][i][d] * sc;
       den += sm_l[w][i] * sc;
     }
-    Store<T>::st(static_cast<T*>(a.out) + (((size_t)b * a.T + t) * a.Hq + h * g + j) * dh + d,
-                 num / den);
+    static_cast<float*>(a.out)[(((size_t)b * a.T + t) * a.Hq + h * g + j) * dh + d] = num / den;
   }
-}
-
-template <typename T, typename C>
-void launch(const TreeAttnArgs& a, cudaStream_t stream) {
-  const int rows = a.T * (a.Hq / a.Hkv);
-  const int grid = a.B * a.Hkv * ((rows + kQG - 1) / kQG);
-  if (a.dh == 64)
-    tree_simt<T, C, 2><<<grid, kNW * 32, 0, stream>>>(a);
-  else
-    tree_simt<T, C, 4><<<grid, kNW * 32, 0, stream>>>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_simt(const TreeAttnArgs& a, cudaStream_t stream) {
-  if (a.dtype == FDLLM_F32)
-    launch<float, float>(a, stream);
-  else if (a.fp8)
-    launch<__nv_bfloat16, uint8_t>(a, stream);
+  const int rows = a.T * (a.Hq / a.Hkv);
+  const int grid = a.B * a.Hkv * ((rows + kQG - 1) / kQG);
+  if (a.dh == 64)
+    tree_simt<2><<<grid, kNW * 32, 0, stream>>>(a);
   else
-    launch<__nv_bfloat16, __nv_bfloat16>(a, stream);
+    tree_simt<4><<<grid, kNW * 32, 0, stream>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
