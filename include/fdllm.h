@@ -271,7 +271,9 @@ fdllm_status fdllm_track_select(int B, int N, int H, int dh, int nq, int dtype,
  * write the drafts' k,v behind the sequence (fdllm_cache_write_fp8 or its own
  * 16-bit write), attend the tree (fdllm_tree_attend*), form the target's
  * probabilities, verify (fdllm_chain_verify / fdllm_tree_verify), and write the
- * accepted nodes' k,v at the slots they end up in.
+ * accepted nodes' k,v at the slots they end up in.  One workspace of the largest
+ * size serves all of these calls in turn; those of the calls above lay theirs out
+ * in other ways.
  * ------------------------------------------------------------------------- */
 
 /* Workspace of the two calls below (the status header alone; B, R >= 0). */

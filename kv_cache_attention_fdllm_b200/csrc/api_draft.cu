@@ -41,15 +41,18 @@ fdllm_status check_draft(int B, int T, int V, int most) {
   return FDLLM_OK;
 }
 
-// [header | one counter a sequence | sums]
-constexpr size_t kVerifyPartsOff = kWsHeaderBytes + kMaxVerifySeqs * sizeof(unsigned);
+// Workspaces: [header | counters, zero between calls | what a call leaves behind].  The
+// counters lie at the same place for attention and verification, whatever the shapes are:
+// neither writes where the other expects zeros.
+constexpr size_t kCountersOff = kWsHeaderBytes;
+constexpr size_t kScratchOff = kCountersOff + kMaxVerifySeqs * sizeof(unsigned);
 
-size_t draft_verify_bytes(int B, int V) { return kVerifyPartsOff + draft_verify_parts_bytes(B, V); }
+size_t draft_verify_bytes(int B, int V) { return kScratchOff + draft_verify_parts_bytes(B, V); }
 
 void set_verify_ws(DraftVerifyArgs* a, void* ws) {
   a->status = reinterpret_cast<int*>(ws);
-  a->seq_cnt = reinterpret_cast<unsigned*>(ws_at(ws, kWsHeaderBytes));
-  a->parts = reinterpret_cast<double*>(ws_at(ws, kVerifyPartsOff));
+  a->seq_cnt = reinterpret_cast<unsigned*>(ws_at(ws, kCountersOff));
+  a->parts = reinterpret_cast<double*>(ws_at(ws, kScratchOff));
 }
 
 fdllm_status run_tree(const TreeAttnArgs& args, void* workspace, size_t workspace_bytes,
@@ -66,8 +69,11 @@ fdllm_status run_tree(const TreeAttnArgs& args, void* workspace, size_t workspac
   if ((a.parent && !aligned16(a.parent)) || (a.n_nodes && !aligned16(a.n_nodes)))
     return FDLLM_ERR_INVALID_ARG;
   a.status = reinterpret_cast<int*>(workspace);
-  a.ws = ws_at(workspace, kWsHeaderBytes);
-  a.ws_bytes = need - kWsHeaderBytes;
+  if (a.dtype != FDLLM_F32) {
+    a.cnt = reinterpret_cast<unsigned*>(ws_at(workspace, kCountersOff));
+    a.ws = ws_at(workspace, kScratchOff);
+    a.ws_bytes = need - kScratchOff;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return from_cuda(a.dtype == FDLLM_F32 ? launch_tree_simt(a, s) : launch_tree_tc(a, s));
 }
@@ -127,7 +133,7 @@ fdllm_status fdllm_cache_read_fp8(int B, int N, int H, int dh, int R, int dtype,
 size_t fdllm_tree_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int dh, int T, int dtype) {
   if (check_tree(B, N, Hq, Hkv, dh, T, dtype) != FDLLM_OK) return 0;
   if (dtype == FDLLM_F32) return kWsHeaderBytes;
-  return kWsHeaderBytes + tree_tc_workspace_bytes(Hq, Hkv, dh, T, device_sm_count());
+  return kScratchOff + tree_tc_workspace_bytes(Hq, Hkv, dh, T, device_sm_count());
 }
 
 fdllm_status fdllm_tree_attend(int B, int N, int Hq, int Hkv, int dh, int T, int dtype,

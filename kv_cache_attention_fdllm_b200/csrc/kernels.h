@@ -139,9 +139,11 @@ struct TreeAttnArgs {
   const int32_t* n_nodes;   // [B] or null (T)
   void* out;                // [B, T, Hq*dh]
   int* status;
+  unsigned* cnt;            // [kTreeCounters], zero between calls (16 and 8 bits)
   void* ws;
   size_t ws_bytes;
 };
+constexpr int kTreeCounters = 1024;  // one a CTA
 cudaError_t launch_tree_simt(const TreeAttnArgs& a, cudaStream_t stream);  // fp32
 cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream);    // 16 and 8 bits
 size_t tree_tc_workspace_bytes(int Hq, int Hkv, int dh, int T, int num_sms);
@@ -163,9 +165,10 @@ struct DraftVerifyArgs {
   unsigned* seq_cnt;        // [kMaxVerifySeqs], zero between calls
   double* parts;            // [B][sub-blocks of a row]
 };
-// Sequences of one call.  The counters have their place whatever the shapes are,
-// so that calls of different shapes share a workspace.
+// Sequences of one call.  The counters have their place whatever the shapes are, in front
+// of what else the calls for drafted tokens keep there, so that all of them share a workspace.
 constexpr int kMaxVerifySeqs = 16384;
+static_assert(kTreeCounters <= kMaxVerifySeqs, "the same counters");
 size_t draft_verify_parts_bytes(int B, int V);
 cudaError_t launch_chain_verify(const DraftVerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_verify(const DraftVerifyArgs& a, cudaStream_t stream);

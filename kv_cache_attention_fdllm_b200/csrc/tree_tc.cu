@@ -70,7 +70,6 @@ constexpr int kMaxNodes = FDLLM_MAX_TREE_NODES;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -3.0e38f;  // maximum of a row that has seen no slot yet (finite: a
                                    // masked score, -inf, then weighs 2^-inf = 0, not NaN)
-constexpr int kMaxGrid = 1024;     // counters: one a CTA
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr size_t kSmemBudget = 227 * 1024;
 
@@ -90,7 +89,7 @@ struct TreeParams {
   const int32_t* n_nodes;
   __nv_bfloat16* out;
   int* status;
-  unsigned* cnt;        // [kMaxGrid], zero between calls
+  unsigned* cnt;        // [kTreeCounters], zero between calls
   float* partials;      // [grid][2][part_floats]
 };
 
@@ -1543,9 +1542,8 @@ struct TreePlan {
 };
 
 // Rows of an item: the smallest instance that takes them all, else chunks of 64 (of
-// whole nodes).  8 bits: chunks of 32.  (16 columns of one-byte P have no swizzled
-// layout; at 64 one group of 16 warps took 5000 cycles a tile against 2 x 1400 for two
-// chunks of 32.)
+// whole nodes).  8 bits: chunks of 32.  (At 64 the parts' columns leave TMEM room for one
+// group only: 5000 cycles a tile against 2 x 2000 for two chunks of 32.)
 TreePlan plan(const TreeAttnArgs& a, int num_sms) {
   TreePlan q{};
   const int g = a.Hq / a.Hkv, rows = a.T * g;
@@ -1623,12 +1621,12 @@ size_t tree_tc_workspace_bytes(int Hq, int Hkv, int dh, int T, int num_sms) {
   const int rows = T * (Hq / Hkv);
   const int NQ = rows <= 32 ? 32 : (rows <= 48 ? 48 : 64);
   const size_t floats = part_floats(NQ, dh);
-  return kMaxGrid * sizeof(unsigned) + align_up((size_t)num_sms * 2 * floats * sizeof(float), 256);
+  return align_up((size_t)num_sms * 2 * floats * sizeof(float), 256);
 }
 
 cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream) {
   const int sms = device_sm_count();
-  if (sms > kMaxGrid) return cudaErrorInvalidValue;
+  if (sms > kTreeCounters) return cudaErrorInvalidValue;
   const TreePlan q = plan(a, sms);
   if (q.nk < 2 || q.nv < 2) return cudaErrorInvalidValue;
   if (tree_tc_workspace_bytes(a.Hq, a.Hkv, a.dh, a.T, sms) > a.ws_bytes) return cudaErrorInvalidValue;
@@ -1668,8 +1666,8 @@ cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream) {
   prm.cache_len = a.cache_len; prm.parent = a.parent; prm.n_nodes = a.n_nodes;
   prm.out = static_cast<__nv_bfloat16*>(a.out);
   prm.status = a.status;
-  prm.cnt = static_cast<unsigned*>(a.ws);
-  prm.partials = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kMaxGrid * sizeof(unsigned));
+  prm.cnt = a.cnt;
+  prm.partials = static_cast<float*>(a.ws);
 #define FDLLM_TREE_CASE(NQv, DHv, FP8v) \
   if (q.NQ == NQv && a.dh == DHv && (a.fp8 != 0) == FP8v) return launch_t<NQv, DHv, FP8v>(q, prm, maps, stream);
   FDLLM_TREE_CASE(16, 64, false)
