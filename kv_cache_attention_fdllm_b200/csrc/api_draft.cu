@@ -75,7 +75,7 @@ fdllm_status run_tree(const TreeAttnArgs& args, void* workspace, size_t workspac
     a.ws_bytes = need - kScratchOff;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return from_cuda(a.dtype == FDLLM_F32 ? launch_tree_simt(a, s) : launch_tree_tc(a, s));
+  return from_cuda(tree_simt_takes(a) ? launch_tree_simt(a, s) : launch_tree_tc(a, s));
 }
 
 }  // namespace

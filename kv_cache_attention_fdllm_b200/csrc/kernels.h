@@ -144,8 +144,9 @@ struct TreeAttnArgs {
   size_t ws_bytes;
 };
 constexpr int kTreeCounters = 1024;  // one a CTA
-cudaError_t launch_tree_simt(const TreeAttnArgs& a, cudaStream_t stream);  // fp32
-cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream);    // 16 and 8 bits
+bool tree_simt_takes(const TreeAttnArgs& a);  // fp32, and few rows of 16 and 8 bits
+cudaError_t launch_tree_simt(const TreeAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_tc(const TreeAttnArgs& a, cudaStream_t stream);  // 16 and 8 bits
 size_t tree_tc_workspace_bytes(int Hq, int Hkv, int dh, int T, int num_sms);
 
 // ----------------------------------------------------------------- sampled verification

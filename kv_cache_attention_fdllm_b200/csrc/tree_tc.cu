@@ -46,7 +46,7 @@
 //
 // Instructions are the other bound in 8 bits: what a CTA does once a segment (open, close,
 // merge, write) runs from cold instruction caches, so rare and once-a-segment code is kept
-// out of line and short there.  In 16 bits the same calls cost single tokens 2 us of 22.
+// out of line and short there.  In 16 bits the same calls cost short items 2 us of 22.
 //
 // NaN and infinity.  Slots past the sequence's nodes are masked in S and zeroed in V
 // (0 x NaN would be NaN).  A node's V that is not finite is zeroed the same way, since
@@ -97,8 +97,8 @@ template <int NQ, int DH, bool FP8>
 struct Cfg {
   // Softmax threads.  Two groups that take turns at the tiles where a tile's way through
   // one (scores, maximum, weights, each behind a wait) takes longer than its bytes: in 8
-  // bits, and in the latency of the few rows of single tokens (measured at 16 rows, one
-  // sequence: 22.9 us with one group, 20.0 with two).  Else one group with more registers
+  // bits, and in the latency of few rows (measured at 16 rows, one sequence: 22.9 us with
+  // one group, 20.0 with two).  Else one group with more registers
   // (32 rows, 64 sequences of 4096: 712 us with two groups, 685 with one).
   static constexpr int kGroups = (FP8 || NQ <= 16) ? 2 : 1;
   static constexpr int kCols = 16;  // rows of a thread
@@ -447,7 +447,7 @@ __device__ __forceinline__ void build_seen_here(const TreeParams& p, int node0, 
 }
 
 // The two out of line in 8 bits (136 us for 141 of 32 rows over 64 sequences of 4096), in
-// line in 16 (a single token: 22.5 us for 24.4).
+// line in 16 (one row, one sequence of 1024: 22.5 us for 24.4).
 template <bool FP8>
 __device__ __noinline__ bool clean_v_out(uint8_t* at, bool none, int row, int boxes, int box) {
   return clean_v_here<FP8>(at, none, row, boxes, box);

@@ -331,3 +331,64 @@ def test_offsets_past_32_bits(F):
         assert F.fdllm_get_status(ws) == F.OK
         outs.append(out)
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,T", [
+    (1, 1, 1, 1), (4, 4, 4, 1), (4, 4, 2, 1), (4, 6, 2, 1), (4, 8, 2, 1), (4, 2, 2, 2), (4, 2, 1, 2), (4, 3, 3, 3),
+    (4, 2, 2, 4), (9, 8, 8, 1), (40, 3, 3, 1), (100, 3, 3, 1), (40, 8, 2, 1)])
+def test_few_rows(F, kind, dh, B, Hq, Hkv, T):
+    """Up to 4 rows to a kv head, over lengths from none to several rounds of every part."""
+    N = 2600
+    some = [N - T, 0, 129, 1, 16, 517, 64, 255, 1024]
+    lens = [some[b % len(some)] for b in range(B)]
+    nodes = None if T == 1 else [T - b % 3 if T > b % 3 else 0 for b in range(B)]
+    c = Case(kind, B, N, Hq, Hkv, dh, T, lens, parent="roots", nodes=nodes, seed=dh + T).dev(F)
+    c.call(F)
+    c.check()
+    assert F.fdllm_get_status(c.ws) == F.OK
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_single_tokens_captured_on_growing_lengths(F, kind):
+    """One token at a time: the call is captured once, the lengths grow on the device."""
+    c = Case(kind, 2, 600, 4, 2, 128, 1, [3, 500], parent=None, seed=21).dev(F)
+    for t in (c.t["k"], c.t["v"]) + tuple(c.t["scales"] or ()):  # no slot is out of use for good
+        x = t.view(torch.uint8) if t.element_size() == 1 else t
+        x[:, :, 3:] = x[:, :, :1]
+    host = lambda t: O.e4m3_to_f64(t.view(torch.uint8).cpu().numpy()) if kind == "fp8" else O.to_f64(t.cpu())  # noqa: E731
+    c.k64, c.v64 = host(c.t["k"]), host(c.t["v"])
+    if kind == "fp8":
+        c.k64, c.v64 = (x * s.cpu().numpy()[..., None].astype(np.float64) for x, s in zip((c.k64, c.v64), c.t["scales"]))
+    c.call(F)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call(F)
+        c.t["lens"] += 1
+    for _ in range(40):
+        graph.replay()
+    c.lens = c.lens + 39
+    c.check()
+    assert F.fdllm_get_status(c.ws) == F.OK
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,Hq", [(1, 2), (1, 8), (9, 8)])
+def test_same_bits_in_any_capacity(F, kind, T, Hq):
+    """The cache's capacity changes no bit of the result."""
+    outs = []
+    for N in (300, 9000):
+        c = Case(kind, 2, 300, Hq, 2, 64, T, [123, 290], parent=None, seed=8)
+        if N > 300:
+            grow = lambda x: torch.cat([x.view(torch.uint8) if kind == "fp8" and x.dim() == 4 else x,  # noqa: E731
+                                        torch.zeros((2, 2, N - 300) + x.shape[3:], dtype=torch.uint8 if kind == "fp8" and x.dim() == 4 else x.dtype)], 2)
+            back = lambda x: grow(x).view(x.dtype)  # noqa: E731
+            c.k, c.v, c.N = back(c.k), back(c.v), N
+            if c.scales is not None:
+                c.scales = [back(s) for s in c.scales]
+        c.dev(F).call(F)
+        torch.cuda.synchronize()
+        assert F.fdllm_get_status(c.ws) == F.OK
+        outs.append(c.t["out"].cpu())
+    assert torch.equal(outs[0], outs[1])
