@@ -5,7 +5,9 @@ takes torch CUDA tensors, checks their dtype, shape, device and contiguity,
 passes raw pointers and the current CUDA stream, and raises FdllmError on a
 non-OK status.  The library launches on the current CUDA device, so the tensors
 and the stream must be on it (a ValueError otherwise).  Every step of the
-computation runs in the CUDA library.
+computation runs in the CUDA library.  The calls for drafted tokens, where host
+time counts, are checked and made in C++ when they fit (_fast); what does not
+fit comes back to the checks here, which say why.
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import ctypes
 
 import torch
 
+from . import _fast
 from ._native import lib
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_BAD_INDEX, ERR_TIMEOUT, ERR_WORKSPACE = range(7)
@@ -388,6 +391,11 @@ def fdllm_cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scal
 
     k_rows, v_rows [B, R, H, dh]; pos int32 [B, R], -1 skips a row; the caches
     float8_e4m3fn [B, H, N, dh] with float32 scales [B, H, N], updated in place."""
+    if stream is None:
+        st = _fast.cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
+        if st >= 0:
+            _check(st, "fdllm_cache_write_fp8")
+            return
     B, N, H, dh, R = _check_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
     st = lib().fdllm_cache_write_fp8(B, N, H, dh, R, _dtype_code(k_rows), _at(k_rows), _at(v_rows),
                                      _at(pos), _at(k_cache), _at(v_cache), _at(k_scale), _at(v_scale),
@@ -399,6 +407,11 @@ def fdllm_cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scal
 def fdllm_cache_read_fp8(pos, k_cache, v_cache, k_scale, v_scale, k_rows, v_rows, workspace,
                          stream=None):
     """Rows of an 8-bit cache read back into k_rows, v_rows [B, R, H, dh] (see include/fdllm.h)."""
+    if stream is None:
+        st = _fast.cache_read_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
+        if st >= 0:
+            _check(st, "fdllm_cache_read_fp8")
+            return k_rows, v_rows
     B, N, H, dh, R = _check_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
     st = lib().fdllm_cache_read_fp8(B, N, H, dh, R, _dtype_code(k_rows), _at(pos), _at(k_cache),
                                     _at(v_cache), _at(k_scale), _at(v_scale), _at(k_rows), _at(v_rows),
@@ -434,8 +447,13 @@ def fdllm_tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, work
 
     q [B, T, Hq, dh]; caches [B, Hkv, N, dh]; cache_len int32 [B]; parent int32
     [B, T] or None (a chain); n_nodes int32 [B] or None (T); out [B, T, Hq*dh]."""
-    B, N, Hq, Hkv, dh, T = _check_tree(q, k_cache, v_cache, q.dtype, cache_len, parent, n_nodes,
-                                       out, workspace)
+    if stream is None:
+        st = _fast.tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, workspace)
+        if st >= 0:
+            _check(st, "fdllm_tree_attend")
+            return out
+    B, N, Hq, Hkv, dh, T = _check_tree(q, k_cache, v_cache, getattr(q, "dtype", None), cache_len,
+                                       parent, n_nodes, out, workspace)
     st = lib().fdllm_tree_attend(B, N, Hq, Hkv, dh, T, _dtype_code(q), _at(q), _at(k_cache),
                                  _at(v_cache), _at(cache_len), _at(parent), _at(n_nodes), _at(out),
                                  _at(workspace), workspace.numel(), _stream_on(stream, q.device))
@@ -446,6 +464,12 @@ def fdllm_tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, work
 def fdllm_tree_attend_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_len, parent, n_nodes, out,
                           workspace, stream=None):
     """fdllm_tree_attend over an 8-bit cache (float8_e4m3fn, float32 scales [B, Hkv, N])."""
+    if stream is None:
+        st = _fast.tree_attend_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_len, parent,
+                    n_nodes, out, workspace)
+        if st >= 0:
+            _check(st, "fdllm_tree_attend_fp8")
+            return out
     B, N, Hq, Hkv, dh, T = _check_tree(q, k_cache, v_cache, torch.float8_e4m3fn, cache_len, parent,
                                        n_nodes, out, workspace)
     _need(k_scale, "k_scale", torch.float32, (B, Hkv, N), q.device)
@@ -465,6 +489,11 @@ def fdllm_chain_verify(target, draft, tok, n_draft, u, r, n_accept, next_tok, wo
     target float32 [B, T+1, V], draft float32 [B, T, V], tok int32 [B, T], n_draft
     int32 [B] or None (T), u float32 [B, T], r float32 [B]; n_accept, next_tok
     int32 [B] (out)."""
+    if stream is None:
+        st = _fast.chain_verify(target, draft, tok, n_draft, u, r, n_accept, next_tok, workspace)
+        if st >= 0:
+            _check(st, "fdllm_chain_verify")
+            return n_accept, next_tok
     _need(target, "target", torch.float32)
     _dims(target, "target", 3)
     _need(draft, "draft", torch.float32)
@@ -495,6 +524,12 @@ def fdllm_tree_verify(target, tok, parent, n_nodes, u, r, path, n_accept, next_t
     target float32 [B, T, V], tok and parent int32 [B, T], n_nodes int32 [B] or
     None (T), u float32 [B, T], r float32 [B]; path int32 [B, T], n_accept and
     next_tok int32 [B] (out)."""
+    if stream is None:
+        st = _fast.tree_verify(target, tok, parent, n_nodes, u, r, path, n_accept, next_tok,
+                    workspace)
+        if st >= 0:
+            _check(st, "fdllm_tree_verify")
+            return path, n_accept, next_tok
     _need(target, "target", torch.float32)
     _dims(target, "target", 3)
     B, T, V = target.shape

@@ -1,4 +1,5 @@
-"""Builds libfdllm.so in-tree from csrc/*.cu for sm_100a with nvcc.
+"""Builds libfdllm.so in-tree from csrc/*.cu for sm_100a with nvcc, and the binding's
+short way to it (_fast, csrc/fast_call.cpp) with the host compiler against torch's headers.
 
 Usage: python kv_cache_attention_fdllm_b200/build.py [--force] [-v] [--ptxas]
 (run it by path: importing the package itself requires the built library)
@@ -8,10 +9,12 @@ next to this file so that it travels with the source tree.
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfdllm.so")
+FAST = os.path.join(PKG, "_fast.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -43,8 +47,21 @@ def _headers_mtime():
     return max((os.path.getmtime(h) for h in hs), default=0.0)
 
 
+def _fast_command(cc) -> list:
+    # found, not imported: importing torch takes longer than the compilation it is for
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(cc)), "include")
+    libs = os.path.join(torch, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", os.path.join(CSRC, "fast_call.cpp"),
+            "-o", FAST, "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-L", PKG, "-l:libfdllm.so",
+            "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile every kernel source for sm_100a and link libfdllm.so; returns its path."""
+    """Compile every kernel source for sm_100a, link libfdllm.so and _fast.so; returns the
+    former's path."""
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     hdr = _headers_mtime()
@@ -64,7 +81,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {cmd[-3]}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose or ptxas_verbose:
             sys.stdout.write(r.stdout + r.stderr)
         return r
@@ -76,6 +93,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         cmd = [cc] + ARCH + ["-shared", "-o", LIB] + objs + ["-lcudart_static", "-ldl", "-lrt",
                                                                "-lpthread"]
         run(cmd)
+    src = os.path.join(CSRC, "fast_call.cpp")
+    if force or not os.path.exists(FAST) or os.path.getmtime(FAST) < max(os.path.getmtime(src), hdr):
+        run(_fast_command(cc))
     return LIB
 
 
