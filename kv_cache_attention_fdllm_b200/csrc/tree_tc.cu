@@ -139,7 +139,8 @@ struct Misc {
   static constexpr int kInts = 400;             // Ints
   static constexpr int kM = 640;                // by group: m_run[64], alpha[64], alpha_o[64]
   static constexpr int kRed = kM + 2 * 768;     // by group: wred[4][64]
-  static constexpr int kSegM = kRed + 2 * 1024; // seg_m, seg_l [2 O buffers][2 groups][64]
+  static constexpr int kSum = kRed + 2 * 1024;  // by group: lred[4][64]
+  static constexpr int kSegM = kSum + 2 * 1024; // seg_m, seg_l [2 O buffers][2 groups][64]
   static constexpr int kCol = kSegM + 2 * 1024; // col_off[64]: a row's offset in q and out
   static constexpr int kQsc = kCol + 256;       // qsc[2], maxima of Q by warp [16], [2]
   static constexpr int kZero = kQsc + 128;      // [64] zeros
@@ -611,6 +612,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   int* abort_flag = &I->abort;
   float* s_mrun = reinterpret_cast<float*>(misc + Misc::kM);
   float* s_wred = reinterpret_cast<float*>(misc + Misc::kRed);
+  float* s_lred = reinterpret_cast<float*>(misc + Misc::kSum);
   float* seg_m = reinterpret_cast<float*>(misc + Misc::kSegM);
   float* seg_l = seg_m + 2 * 128;
   int* col_off = reinterpret_cast<int*>(misc + Misc::kCol);
@@ -956,6 +958,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     float* alpha = m_run + 64;
     float* alpha_o = alpha + 64;
     float* wred = s_wred + grp * 256;  // [4][64]
+    // a segment's sums of l by warp.  Not in wred's place: the next segment's first tile
+    // writes there without a barrier behind the reads of these
+    float* lred = s_lred + grp * 256;
     unsigned long long* vis = s_vis + grp * kMaxNodes;
     int* par = s_par + grp * kMaxNodes;
     float l[NQH];
@@ -1345,14 +1350,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           }
         }
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
-        if (!(lane & 1)) wred[quarter * 64 + c0 + (lane >> 1)] = l[0];
+        if (!(lane & 1)) lred[quarter * 64 + c0 + (lane >> 1)] = l[0];
         tc::named_bar_sync(bar_a, GT);
       }
       const int sl = seg & 1;
       if (gt < NQ) {
         seg_m[sl * 128 + grp * 64 + gt] = last >= 0 ? m_run[gt] : kNone;
         seg_l[sl * 128 + grp * 64 + gt] =
-            last >= 0 ? wred[gt] + wred[64 + gt] + wred[128 + gt] + wred[192 + gt] : 0.f;
+            last >= 0 ? lred[gt] + lred[64 + gt] + lred[128 + gt] + lred[192 + gt] : 0.f;
       }
       if (gt == 0) {
         I->seg_has[sl][grp] = last >= 0;

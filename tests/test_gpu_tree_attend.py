@@ -392,3 +392,22 @@ def test_same_bits_in_any_capacity(F, kind, T, Hq):
         assert F.fdllm_get_status(c.ws) == F.OK
         outs.append(c.t["out"].cpu())
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("kind,Hq,Hkv,T", [
+    ("bf16", 64, 16, 4), ("bf16", 64, 16, 7), ("bf16", 48, 16, 15), ("bf16", 64, 16, 50), ("fp8", 64, 16, 3),
+    ("fp8", 48, 16, 15)])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_many_short_items_are_the_same_every_time(F, kind, Hq, Hkv, T, dh):
+    """A CTA that goes through many items hands its sums over between them: the end of one
+    and the first tile of the next do not meet in shared memory."""
+    B, N = 32, 700
+    lens = [(b * 97) % (N - T) for b in range(B)]
+    c = Case(kind, B, N, Hq, Hkv, dh, T, lens, seed=4).dev(F)
+    c.call(F)
+    c.check(seqs=[1, 17])
+    first = c.t["out"].clone()
+    for _ in range(30):
+        c.t["out"].fill_(MARK)
+        c.call(F)
+        assert torch.equal(c.t["out"].view(torch.int16), first.view(torch.int16))
