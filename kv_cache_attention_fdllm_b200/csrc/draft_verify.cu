@@ -19,7 +19,10 @@
 // (all gathers at once, then shared memory), which costs less than a second
 // launch; its warps then sum sub-blocks of 512 weights, 16-byte loads all in
 // flight before the first is used; the last CTA of the sequence to finish finds
-// the sub-block that holds r sum(w) from the sums, and in it the token.
+// the sub-block that holds r sum(w) from the sums, and in it the token.  Measured at a
+// vocabulary of 126464: 8 chains of 5 drafts 8.2 us, 64 of 4 16.5 us (64.8 MB), 8 trees of
+// 40 nodes 10.2 us; of the 8.2 us the walk takes 1.5, the sums 2.6, the count 1, the draw
+// 2.8, each a dependent round trip or two.
 #include <limits.h>
 
 #include "common.cuh"
