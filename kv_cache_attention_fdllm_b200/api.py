@@ -15,8 +15,13 @@ import ctypes
 
 import torch
 
-from . import _fast
 from ._native import lib
+
+try:
+    from . import _fast
+except ImportError as e:
+    raise ImportError("_fast.so is missing or was built for another torch: build it with "
+                      "`python kv_cache_attention_fdllm_b200/build.py`") from e
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_BAD_INDEX, ERR_TIMEOUT, ERR_WORKSPACE = range(7)
 FLAG_COMMIT, FLAG_ACCEPT, FLAG_PASS = 1, 2, 4
