@@ -297,10 +297,11 @@ __device__ __noinline__ void add_unfit(const TreeParams& p, int qc, int b, int h
 // A chunk's Q (bf16; `q`: its first row, the others at col_off, ncol in all) as two e4m3
 // parts: q 2^sh = q1 + q2 with the chunk's largest in [128, 256), so that what is lost is
 // below 2^-17 of it.  Rows past ncol become zeros.  Warp w of W takes every W-th row, up to
-// 16 rows' loads in flight together; `share`: the maximum over the warps.  Returns 2^-sh.
-template <int NQ, int DH, int W, typename Share>
+// 16 rows' loads in flight together; `share`: the maximum over the warps; `free`: waits until
+// dst may be written.  Returns 2^-sh.
+template <int NQ, int DH, int W, typename Share, typename Free>
 __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_off, int ncol, int w,
-                                         uint8_t* dst, Share share) {
+                                         uint8_t* dst, Share share, Free free) {
   constexpr int R = NQ / W;   // rows of a warp
   constexpr int E = DH / 32;  // elements of a lane
   constexpr uint32_t kPart = NQ * DH;
@@ -347,6 +348,7 @@ __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_
   int sh = 7 - ((int)(mx >> 7) - 127);
   sh = mx == 0u ? 0 : min(max(sh, -120), 120);
   const float up = __int_as_float((127 + sh) << 23);
+  free();
 #pragma unroll 1
   for (int x0 = 0; x0 < R; x0 += N) {
     if (x0) {
@@ -1091,7 +1093,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (lane == 0) w_max[warp - C::kFirst] = (int)mx;
             tc::named_bar_sync(kBarAll, C::kSmx);
             return __reduce_max_sync(0xffffffffu, (uint32_t)w_max[lane & (C::kSmx / 32 - 1)]);
-          });
+          },
+          [] {});
       if (st == 0) qsc[0] = unit;
       tc::fence_proxy_async_smem();
       tc::named_bar_sync(kBarAll, C::kSmx);
@@ -1486,7 +1489,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       for (int n = 1; left > 0; ++n) {
         const int qb = n & 1;
         cq.next_item(S);
-        wait_bar(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status);
         const float unit = split_q<NQ, DH, 2>(
             static_cast<const __nv_bfloat16*>(p.q) + row_of(cq.qc, cq.b, cq.h), col_off,
             columns(cq.qc, cq.b), warp - 2, q_buf + qb * C::kQParts * C::kQPart, [&](uint32_t mx) {
@@ -1494,7 +1496,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               if (lane == 0) w_max[warp - 2] = (int)mx;
               tc::named_bar_sync(7, 64);
               return (uint32_t)max(w_max[0], w_max[1]);
-            });
+            },
+            [&] { wait_bar(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status); });
         if (warp == 2 && lane == 0) qsc[qb] = unit;
         tc::fence_proxy_async_smem();
         __syncwarp();
