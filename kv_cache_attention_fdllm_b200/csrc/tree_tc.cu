@@ -44,8 +44,8 @@
 // Measured (head size 128, times of calls back to back).  16 bits: 64 sequences of 4096, 32
 // heads of 32 nodes, 4.3 GB: 650-713 us, the memory's rate; 8 of up to 2000, 32 heads of 40
 // nodes, 239 MB: 60 us, of which 37 are bytes and the rest a CTA's first tile, its two segment
-// ends and merges.  8 bits, 8 kv heads of 32 rows: 64 sequences of 1000-4080, 343 MB: 131 us;
-// 8 of 16384, 278 MB: 90 us: 2000-2300 cycles a tile, some 10000 more a segment.
+// ends and merges.  8 bits, 8 kv heads of 32 rows: 64 sequences of 1000-4080, 343 MB: 129 us;
+// 8 of 16384, 278 MB: 89 us: 2000-2300 cycles a tile, some 10000 more a segment.
 //
 // O^T is double-buffered in TMEM (once for each group): an item's result is written
 // some tiles into the next item, off the softmax path.
@@ -205,12 +205,6 @@ __device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, float* v, int w) {
   else
     tc::tmem_ld8(taddr, v);
 }
-__device__ __forceinline__ void tmem_st_chunk(uint32_t taddr, const float* v, int w) {
-  if (w >= 16)
-    tc::tmem_st16(taddr, v);
-  else
-    tc::tmem_st8(taddr, v);
-}
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -317,12 +311,14 @@ __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_
     }
     return raw;
   };
-  // at most 16 rows in registers: a warp's other rows are read twice
-  constexpr int N = R < 16 ? R : 16;
-  uint2 raw[N];
+  // Two passes, the second of which finds the rows in L1: registers for all of them would
+  // unroll the conversions, 11 KB of code that the softmax warps' then has to make room for
+  // (64 sequences of 500: 65 us for 71)
+  constexpr int N = R < 16 ? R : 16, M = R < 2 ? R : 2;
   uint32_t m2 = 0u;  // two maxima
 #pragma unroll 1
-  for (int x0 = R - N; x0 >= 0; x0 -= N) {
+  for (int x0 = 0; x0 < R; x0 += N) {
+    uint2 raw[N];
 #pragma unroll
     for (int x = 0; x < N; ++x) raw[x] = load(w + (x0 + x) * W);
 #pragma unroll
@@ -335,6 +331,7 @@ __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_
   const bool odd = mx >= 0x7f80u;
   if (odd) {
     mx = 0u;
+#pragma unroll 1
     for (int r = w; r < NQ; r += W) {
       const uint2 v = load(r);
 #pragma unroll
@@ -350,13 +347,12 @@ __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_
   const float up = __int_as_float((127 + sh) << 23);
   free();
 #pragma unroll 1
-  for (int x0 = 0; x0 < R; x0 += N) {
-    if (x0) {
+  for (int x0 = 0; x0 < R; x0 += M) {
+    uint2 raw[M];
 #pragma unroll
-      for (int x = 0; x < N; ++x) raw[x] = load(w + (x0 + x) * W);
-    }
+    for (int x = 0; x < M; ++x) raw[x] = load(w + (x0 + x) * W);
 #pragma unroll
-    for (int x = 0; x < N; ++x) {
+    for (int x = 0; x < M; ++x) {
       const int r = w + (x0 + x) * W;
       uint32_t b1 = 0u, b2 = 0u;
 #pragma unroll
@@ -513,19 +509,6 @@ struct IdleClock {
     return true;
   }
 };
-
-// Spins on a barrier's phase with the whole warp (a suspended wait wakes up late); false
-// after kWaitLimitNs.
-__device__ __noinline__ bool spin_on(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  IdleClock clk;
-  while (!__all_sync(kFull, tc::mbar_test(bar, parity)))
-    if (__any_sync(kFull, !clk.idle(abort, status))) return false;
-  return true;
-}
-__device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  if (__all_sync(kFull, tc::mbar_test(bar, parity))) return true;
-  return spin_on(bar, parity, abort, status);
-}
 
 // First unit of CTA c's range, and the CTA whose range holds unit u (the largest c
 // with lo(c) <= u; a double-precision estimate is put right with exact products).
@@ -1395,6 +1378,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
     // ---- the finisher has taken the counts of this CTA's partials
     tc::named_bar_sync(kBarCount, C::kSmx + 32);
+#pragma unroll 1
     for (int slot = 0; slot < 2; ++slot) {
       const int iu = I->merge_u[slot];
       if (iu < 0) continue;
@@ -1512,6 +1496,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         Cursor ca, cz;
         ca.init(u0, S);
         cz.init(u1 - 1, S);
+#pragma unroll 1
         for (int slot = 0; slot < 2; ++slot) {
           const int iu = slot == 0 ? u0 - ca.t : u1 - 1 - cz.t;
           const int tb = slot == 0 ? ca.tb : cz.tb;
