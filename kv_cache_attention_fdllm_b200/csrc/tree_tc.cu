@@ -20,8 +20,10 @@
 //   - a weight is taken as three e5m2 parts (3 significant bits each, of its fp16
 //     value): 9 bits, as bf16 has 8, over a range of 2^31, so that a long flat rest
 //     far below a sink keeps its weight.  e4m3 parts would lose it (2^17).  The
-//     weights carry the slot's scale relative to a power of two that follows the
-//     scales as the running maximum follows the scores.
+//     weights carry the slot's scale, and the running maximum of a row is that of
+//     score + log2 of the scale over the slots it sees: its largest product of a weight
+//     and a scale uses the range, whatever other rows see, and what is lost of a slot is
+//     below 2^-25 of that product.
 // The parts are more columns of the same MMAs, and an MMA takes some 80 cycles (its
 // 128 x 32 bytes of A) whatever its columns: a tile's 8 take about half of the 1400
 // cycles that its bytes take from HBM.  (As separate products they took 20.)
@@ -129,11 +131,11 @@ struct Cfg {
   static constexpr int kOCols = FP8 ? 3 * NQ : kNQP;
   static constexpr uint32_t kPRow = FP8 ? 128 : kNQP * 2;  // bytes of a slot in P
   static constexpr uint32_t kPBuf = kKT * kPRow;           // a multiple of 1024
-  // largest exponent step a weight may exceed the running maximum's by, and the
-  // power of two weights are kept at (8 bits: below 2^(6+8+1) in fp16 and e5m2).  A
-  // larger step would rescale less often but leave less room below
-  static constexpr float kThresh = FP8 ? 6.f : 8.f;
-  static constexpr int kPOff = FP8 ? 8 : 0;
+  // A row's largest weight lies at 2^kPOff when its maximum is set, and may grow to 2^kThresh
+  // before it is raised (8 bits, the slot's scale with it: below 2^(14 + 1) in fp16 and
+  // e5m2).  A larger step would rescale less often but leave less room below
+  static constexpr float kThresh = FP8 ? 14.f : 8.f;
+  static constexpr float kPOff = FP8 ? 8.f : 0.f;
   static constexpr int kPartFloats = NQ * DH + 2 * NQ + 4;  // O, m, l, flag (and padding)
 };
 
@@ -143,8 +145,8 @@ struct Cfg {
 struct Misc {
   static constexpr int kBars = 0;               // 50 mbarriers
   static constexpr int kInts = 400;             // Ints
-  static constexpr int kM = 640;                // by group: m_run[64], alpha[64], alpha_o[64]
-  static constexpr int kRed = kM + 2 * 768;     // by group: wred[4][64]
+  static constexpr int kM = 640;                // by group: m_run[64], alpha[64]
+  static constexpr int kRed = kM + 2 * 512;     // by group: wred[4][64]
   static constexpr int kSum = kRed + 2 * 1024;  // by group: lred[4][64]
   static constexpr int kSegM = kSum + 2 * 1024; // seg_m, seg_l [2 O buffers][2 groups][64]
   static constexpr int kCol = kSegM + 2 * 1024; // col_off[64]: a row's offset in q and out
@@ -161,13 +163,11 @@ struct Ints {
   uint32_t tmem;
   int abort;
   int merge_u[2];     // first unit of the item in partial slot s that this CTA merges, or -1
-  // a closed segment, by O buffer and group: has the group tiles in it, the power of two
-  // its weights were taken against, did it meet a node's V that is not finite
+  // a closed segment, by O buffer and group: has the group tiles in it, did it meet a node's
+  // V that is not finite
   int seg_has[2][2];
-  int seg_e[2][2];
   int seg_bad[2][2];
   int bad_run[2];     // the last of the running segment, by group
-  int vexp[2][4];     // by group: exponents of the V scales of a quarter's slots
   // the item of a closed segment, by O buffer and group (every thread of the group writes
   // the same): chunk, sequence, kv head, its first unit, whether the segment is all of it,
   // and the group's last tile in it
@@ -945,9 +945,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int bar_a = 1 + 2 * grp, bar_b = 2 + 2 * grp;  // named barriers of the group
     constexpr int kBarCount = 5, kBarAll = 6;
-    float* m_run = s_mrun + grp * 192;  // [64], then the rescales of l and of O
+    float* m_run = s_mrun + grp * 128;  // [64], then the rescales of l and O
     float* alpha = m_run + 64;
-    float* alpha_o = alpha + 64;
     float* wred = s_wred + grp * 256;  // [4][64]
     // a segment's sums of l by warp.  Not in wred's place: the next segment's first tile
     // writes there without a barrier behind the reads of these
@@ -955,7 +954,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     unsigned long long* vis = s_vis + grp * kMaxNodes;
     int* par = s_par + grp * kMaxNodes;
     float l[NQH];
-    int e_ref = -1000;     // power of two that the segment's weights are taken against
     int vis_key = -1;      // (chunk, sequence) that vis stands for
     int pv_waited = -1;    // index of the last PV this thread waited for
     Cursor cs;
@@ -1002,7 +1000,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // a group without a tile in the segment has left its O as it was
         const bool has = I->seg_has[sl][x] != 0;
         bad |= I->seg_bad[sl][x] != 0;
-        const float unit = FP8 ? exp2f((float)(I->seg_e[sl][x] - C::kPOff)) : 1.f;
         float y[NF], z[C::kOParts > 1 ? 2 * NF : 1];
         const uint32_t at = tmem_o + (uint32_t)((sl * KG + x) * C::kOCols) + lane_off + (uint32_t)f0;
         tmem_ld_chunk(at, y, NF);
@@ -1017,8 +1014,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
 #pragma unroll
         for (int c = 0; c < NF; ++c) {
-          float w = unit;
-          if (KG == 2) w *= ex2_approx(sm[x * 64 + f0 + c] - fmaxf(sm[f0 + c], sm[64 + f0 + c]));
+          float w = 1.f;
+          if (KG == 2) w = ex2_approx(sm[x * 64 + f0 + c] - fmaxf(sm[f0 + c], sm[64 + f0 + c]));
           const float v = has ? y[c] * w : 0.f;
           o[c] = x == 0 ? v : o[c] + v;
         }
@@ -1091,7 +1088,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const int len = s_len[b], lim = len + s_nn[b];
       bool first = true;
       int last = -1;
-      e_ref = -1000;
 #pragma unroll
       for (int c = 0; c < NQH; ++c) l[c] = 0.f;
 #pragma unroll 1
@@ -1113,17 +1109,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const int sb = i & 1;
           wait_bar(&s_full[sb], (uint32_t)(i >> 1) & 1u, abort_flag, p.status);
           tc::tc_fence_after();
-          float ksc = p.qk_scale, vs = 1.f;
+          float ksc = p.qk_scale, vs = 1.f, vexp = 0.f;
           if constexpr (FP8) {
             wait_bar(&v_full[vst], vph, abort_flag, p.status);
             const float* sc = scales + vst * 256 + kl;
             ksc *= sc[0] * qsc[seg & 1];
             vs = sc[128];
+            // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1).  At least 2^-84,
+            // for zeros too (rows all of smaller ones lose bits below 2^-33 of that; l stays
+            // below 2^(14 + 84) a slot); a scale that is not finite weighs nothing here
+            const int eb = (__float_as_int(vs) >> 23) & 255;
+            vexp = (float)(eb < 255 ? max(eb - 127, -84) : -84);
           }
 
           // ---- scores (log2 units) against the running maximum: row kl of S^T, this
-          // thread's columns.  The maximum is raised when a score exceeds it by more than
-          // 2^kThresh (masked scores never do); a segment's first tile sets it.  For that the
+          // thread's columns.  The maximum is raised when a weight (8 bits: times the slot's
+          // scale) exceeds 2^kThresh (masked ones never do); a segment's first tile sets it.  For that the
           // scores are formed again as they are (pass 1): one copy of the code, S being there
           // until the end.
           float d[NQH];  // exponents of the weights
@@ -1158,49 +1159,27 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               for (int c = 0; c < NQH; ++c)
                 if (!((seen >> c) & 1u)) d[c] = -INFINITY;
             }
-            int vexp = -1000;
-            if constexpr (FP8) {
-              // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1), at least
-              // 2^-100; scales of slots that go into no sum, zero ones and those that are
-              // not finite do not count
-              const int eb = (__float_as_int(vs) >> 23) & 255;
-              if (!zero_v && eb > 0 && eb < 255) vexp = max(eb - 127, -100);
-            }
             if (pass == 0) {
               float top = d[0];
 #pragma unroll
               for (int c = 1; c < NQH; ++c) top = fmaxf(top, d[c]);
-              any = bar_any(bar_b, GT, top > C::kThresh || (FP8 && vexp > e_ref));
+              if (FP8) top += vexp;
+              any = bar_any(bar_b, GT, top > C::kThresh);
               if (!any) break;
               pass = 1;
               continue;
             }
 #pragma unroll
             for (int c = 0; c < NQH; ++c) {
-              const float wm = warp_max(d[c]);
+              const float wm = warp_max(FP8 ? d[c] + vexp : d[c]);
               if (lane == c) wred[quarter * 64 + c0 + c] = wm;
             }
-            if constexpr (FP8) {
-              const int e = __reduce_max_sync(0xffffffffu, vexp);
-              if (lane == 0 && c0 == 0) I->vexp[grp][quarter] = e;
-            }
             tc::named_bar_sync(bar_a, GT);
-            float e_scale = 1.f;
-            if constexpr (FP8) {
-              int e_new = e_ref;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) e_new = max(e_new, I->vexp[grp][w]);
-              // 2^(e_ref - e_new): 0 from the start value
-              e_scale = e_ref - e_new < -126 ? 0.f : __int_as_float((e_ref - e_new + 127) << 23);
-              e_ref = e_new;
-            }
             if (gt < NQ) {
               const float mo = first ? kNone : m_run[gt];
               const float tm = fmaxf(fmaxf(wred[gt], wred[64 + gt]), fmaxf(wred[128 + gt], wred[192 + gt]));
-              const float mn = (tm - mo > C::kThresh) ? tm : mo;
-              const float al = ex2_approx(mo - mn);
-              alpha[gt] = al;
-              alpha_o[gt] = al * e_scale;
+              const float mn = (tm - mo > C::kThresh) ? tm - C::kPOff : mo;
+              alpha[gt] = ex2_approx(mo - mn);
               m_run[gt] = mn;
             }
             tc::named_bar_sync(bar_a, GT);
@@ -1230,7 +1209,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               tc::tmem_ld8(at + part * NQ + c1, o);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 8; ++c) o[c] *= alpha_o[c0 + c1 + c];
+              for (int c = 0; c < 8; ++c) o[c] *= alpha[c0 + c1 + c];
               tc::tmem_st8(at + part * NQ + c1, o);
             }
             tc::tmem_wait_st();
@@ -1248,10 +1227,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           // ---- P = 2^(s - m) into row kl of the MN-major swizzled P^T tile
           uint8_t* pb = p_buf + (i & 1) * C::kPBuf;
           if constexpr (FP8) {
-            // the weight carries the slot's scale against 2^e_ref, times 2^kPOff
-            float w = 0.f;
-            if (!zero_v && !(tree && slot >= len && not_finite(vs)))
-              w = vs * __int_as_float((127 + min(C::kPOff - e_ref, 127)) << 23);
+            // the weight carries the slot's scale
+            const float w = zero_v || (tree && slot >= len && not_finite(vs)) ? 0.f : vs;
             uint32_t pk[3][NQH / 4];
 #pragma unroll
             for (int c = 0; c < NQH; c += 4) {
@@ -1353,7 +1330,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       }
       if (gt == 0) {
         I->seg_has[sl][grp] = last >= 0;
-        I->seg_e[sl][grp] = e_ref;
         I->seg_bad[sl][grp] = I->bad_run[grp];
         I->bad_run[grp] = 0;
       }
