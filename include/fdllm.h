@@ -341,7 +341,12 @@ fdllm_status fdllm_tree_attend(int B, int N, int Hq, int Hkv, int dh, int T, int
                                size_t workspace_bytes, void* stream);
 
 /* The same over an 8-bit cache as fdllm_cache_write_fp8 leaves it; q and out
- * bf16 (dtype FDLLM_BF16; fp32 is FDLLM_ERR_UNSUPPORTED). */
+ * bf16 (dtype FDLLM_BF16; fp32 is FDLLM_ERR_UNSUPPORTED).  Precision beyond that of
+ * the 16-bit form, for each (node, head) by itself: an element of q is off by at most
+ * 2^-17 of the largest of its row (on a score: sqrt(dh) 2^-17 max|q| max|k|), and a
+ * slot's weight times its v_scale by 2^-25 of the largest such product among the slots
+ * that the node sees (of 2^-84 times the largest weight where that is more: rows of
+ * v whose elements are all below 2^-75). */
 fdllm_status fdllm_tree_attend_fp8(int B, int N, int Hq, int Hkv, int dh, int T, int dtype,
                                    const void* q, const void* k_cache, const void* v_cache,
                                    const float* k_scale, const float* v_scale,

@@ -15,8 +15,8 @@
 //   - a slot's scale multiplies one row of S^T, i.e. one thread's scores, and for V
 //     the weights of that thread;
 //   - a bf16 query has 8 significant bits, an e4m3 value 4: q 2^x = q1 + q2 with both
-//     e4m3 (x per chunk, so that its largest is in [128, 256)) is exact down to 2^-10,
-//     2^-17 of the largest, and S = K q1 + K q2;
+//     e4m3 (x per row, so that its largest is in [128, 256)) is exact down to 2^-10,
+//     2^-17 of the row's largest, and S = K q1 + K q2, times 2^-x of the column;
 //   - a weight is taken as three e5m2 parts (3 significant bits each, of its fp16
 //     value): 9 bits, as bf16 has 8, over a range of 2^31, so that a long flat rest
 //     far below a sink keeps its weight.  e4m3 parts would lose it (2^17).  The
@@ -150,8 +150,8 @@ struct Misc {
   static constexpr int kSum = kRed + 2 * 1024;  // by group: lred[4][64]
   static constexpr int kSegM = kSum + 2 * 1024; // seg_m, seg_l [2 O buffers][2 groups][64]
   static constexpr int kCol = kSegM + 2 * 1024; // col_off[64]: a row's offset in q and out
-  static constexpr int kQsc = kCol + 256;       // qsc[2], maxima of Q by warp [16], [2]
-  static constexpr int kZero = kQsc + 128;      // [64] zeros
+  static constexpr int kQsc = kCol + 256;       // 8 bits: qsc[2 Q buffers][32], a row's 2^-x
+  static constexpr int kZero = kQsc + 256;      // [64] zeros
   static constexpr int kPar = kZero + 256;      // by group: parents of a sequence's nodes
   static constexpr int kVis = kPar + 2 * kMaxNodes * 4;  // by group: columns that see a node
   static constexpr int kBytes = (kVis + 2 * kMaxNodes * 8 + 1023) / 1024 * 1024;
@@ -289,13 +289,13 @@ __device__ __noinline__ void add_unfit(const TreeParams& p, int qc, int b, int h
 }
 
 // A chunk's Q (bf16; `q`: its first row, the others at col_off, ncol in all) as two e4m3
-// parts: q 2^sh = q1 + q2 with the chunk's largest in [128, 256), so that what is lost is
-// below 2^-17 of it.  Rows past ncol become zeros.  Warp w of W takes every W-th row, up to
-// 16 rows' loads in flight together; `share`: the maximum over the warps; `free`: waits until
-// dst may be written.  Returns 2^-sh.
-template <int NQ, int DH, int W, typename Share, typename Free>
-__device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_off, int ncol, int w,
-                                         uint8_t* dst, Share share, Free free) {
+// parts: q 2^sh = q1 + q2, sh by row so that its largest is in [128, 256): what is lost is
+// below 2^-17 of it, whatever the rows beside it hold.  Rows past ncol become zeros.  Warp w
+// of W takes every W-th row, up to 16 rows' loads in flight together; `free`: waits until dst
+// and unit may be written.  unit takes each row's 2^-sh.
+template <int NQ, int DH, int W, typename Free>
+__device__ __forceinline__ void split_q(const __nv_bfloat16* q, const int* col_off, int ncol, int w,
+                                        uint8_t* dst, float* unit, Free free) {
   constexpr int R = NQ / W;   // rows of a warp
   constexpr int E = DH / 32;  // elements of a lane
   constexpr uint32_t kPart = NQ * DH;
@@ -314,38 +314,26 @@ __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_
   // Two passes, the second of which finds the rows in L1: registers for all of them would
   // unroll the conversions, 11 KB of code that the softmax warps' then has to make room for
   // (64 sequences of 500: 65 us for 71)
-  constexpr int N = R < 16 ? R : 16, M = R < 2 ? R : 2;
-  uint32_t m2 = 0u;  // two maxima
-#pragma unroll 1
-  for (int x0 = 0; x0 < R; x0 += N) {
-    uint2 raw[N];
+  constexpr int M = R < 2 ? R : 2;
+  static_assert(R <= 16, "loads in flight");
+  // lane x keeps the largest |q| of the warp's row x, as the upper 16 bits of a float:
+  // magnitudes compare as whole numbers, what is not finite above all the others
+  uint32_t mx = 0u;
+  {
+    uint2 raw[R];
 #pragma unroll
-    for (int x = 0; x < N; ++x) raw[x] = load(w + (x0 + x) * W);
+    for (int x = 0; x < R; ++x) raw[x] = load(w + x * W);
 #pragma unroll
-    for (int x = 0; x < N; ++x)
-      m2 = __vmaxu2(m2, __vmaxu2(raw[x].x & 0x7fff7fffu, raw[x].y & 0x7fff7fffu));
-  }
-  // the largest |q| as the upper 16 bits of a float: magnitudes compare as whole numbers,
-  // what is not finite above all the others, which then are looked at once more
-  uint32_t mx = share(__reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16)));
-  const bool odd = mx >= 0x7f80u;
-  if (odd) {
-    mx = 0u;
-#pragma unroll 1
-    for (int r = w; r < NQ; r += W) {
-      const uint2 v = load(r);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = ((e < 2 ? v.x : v.y) >> (16 * (e & 1))) & 0x7fffu;
-        if (a < 0x7f80u) mx = max(mx, a);
-      }
+    for (int x = 0; x < R; ++x) {
+      const uint32_t m2 = __vmaxu2(raw[x].x & 0x7fff7fffu, raw[x].y & 0x7fff7fffu);
+      const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+      if (lane == x) mx = m;
     }
-    mx = share(__reduce_max_sync(0xffffffffu, mx));
   }
-  int sh = 7 - ((int)(mx >> 7) - 127);
-  sh = mx == 0u ? 0 : min(max(sh, -120), 120);
-  const float up = __int_as_float((127 + sh) << 23);
+  // of rows of zeros and of those that are not finite: 0
+  int sh = mx == 0u || mx >= 0x7f80u ? 0 : min(max(7 - ((int)(mx >> 7) - 127), -120), 120);
   free();
+  if (lane < R) unit[w + lane * W] = __int_as_float((127 - sh) << 23);
 #pragma unroll 1
   for (int x0 = 0; x0 < R; x0 += M) {
     uint2 raw[M];
@@ -354,16 +342,15 @@ __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_
 #pragma unroll
     for (int x = 0; x < M; ++x) {
       const int r = w + (x0 + x) * W;
+      const float up = __int_as_float((127 + __shfl_sync(0xffffffffu, sh, x0 + x)) << 23);
       uint32_t b1 = 0u, b2 = 0u;
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         const uint32_t q = e < 2 ? raw[x].x : raw[x].y;
         float y0 = __uint_as_float(q << 16) * up, y1 = __uint_as_float(q & 0xffff0000u) * up;
         // what is not finite makes the row NaN (the conversion would saturate it)
-        if (odd) {
-          if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
-          if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
-        }
+        if (not_finite(y0)) y0 = __int_as_float(0x7fffffff);
+        if (not_finite(y1)) y1 = __int_as_float(0x7fffffff);
         const uint32_t q1 = e4m3x2(y0, y1);
         const float2 g1 = from_e4m3x2(q1);
         const uint32_t q2 = e4m3x2(y0 - g1.x, y1 - g1.y);
@@ -380,7 +367,6 @@ __device__ __forceinline__ float split_q(const __nv_bfloat16* q, const int* col_
       }
     }
   }
-  return __int_as_float((127 - sh) << 23);
 }
 
 // A slot's row of V in shared memory (boxes of `row` bytes, `box` bytes apart), behind the
@@ -607,7 +593,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   float* seg_m = reinterpret_cast<float*>(misc + Misc::kSegM);
   float* seg_l = seg_m + 2 * 128;
   int* col_off = reinterpret_cast<int*>(misc + Misc::kCol);
-  float* qsc = reinterpret_cast<float*>(misc + Misc::kQsc);  // [2], then the first split's maxima
+  float* qsc = reinterpret_cast<float*>(misc + Misc::kQsc);  // [2][32]
   float* s_zero = reinterpret_cast<float*>(misc + Misc::kZero);  // [64] zeros
   int* s_par = reinterpret_cast<int*>(misc + Misc::kPar);
   unsigned long long* s_vis = reinterpret_cast<unsigned long long*>(misc + Misc::kVis);
@@ -1065,17 +1051,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint32_t vph = 0u;
     if constexpr (FP8) {
       // the range's first Q is split by all of these warps: nothing else is to do yet
-      int* w_max = reinterpret_cast<int*>(qsc) + 2;
-      const float unit = split_q<NQ, DH, C::kSmx / 32>(
+      split_q<NQ, DH, C::kSmx / 32>(
           static_cast<const __nv_bfloat16*>(p.q) + row_of(cs.qc, cs.b, cs.h), col_off,
-          columns(cs.qc, cs.b), warp - C::kFirst, q_buf, [&](uint32_t mx) {
-            tc::named_bar_sync(kBarAll, C::kSmx);  // a second call's writes come after the reads
-            if (lane == 0) w_max[warp - C::kFirst] = (int)mx;
-            tc::named_bar_sync(kBarAll, C::kSmx);
-            return __reduce_max_sync(0xffffffffu, (uint32_t)w_max[lane & (C::kSmx / 32 - 1)]);
-          },
-          [] {});
-      if (st == 0) qsc[0] = unit;
+          columns(cs.qc, cs.b), warp - C::kFirst, q_buf, qsc, [] {});
       tc::fence_proxy_async_smem();
       tc::named_bar_sync(kBarAll, C::kSmx);
       if (st < 64 && lane == 0) tc::mbar_arrive(&q_full[0]);  // twice
@@ -1113,7 +1091,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           if constexpr (FP8) {
             wait_bar(&v_full[vst], vph, abort_flag, p.status);
             const float* sc = scales + vst * 256 + kl;
-            ksc *= sc[0] * qsc[seg & 1];
+            ksc *= sc[0];
             vs = sc[128];
             // exponent of the slot's V scale: 2^vexp <= |vs| < 2^(vexp + 1).  At least 2^-84,
             // for zeros too (rows all of smaller ones lose bits below 2^-33 of that; l stays
@@ -1140,8 +1118,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
               for (int c = 0; c < NQH; c += 16) tmem_ld_chunk(at + NQ + c, d2 + c, 16);
               tc::tmem_wait_ld();
+              const float4* u4 = reinterpret_cast<const float4*>(qsc + (seg & 1) * 32 + c0);
 #pragma unroll
-              for (int c = 0; c < NQH; ++c) d[c] += d2[c];
+              for (int c = 0; c < NQH; c += 4) {
+                const float4 u = u4[c / 4];
+                d[c] = (d[c] + d2[c]) * u.x;
+                d[c + 1] = (d[c + 1] + d2[c + 1]) * u.y;
+                d[c + 2] = (d[c + 2] + d2[c + 2]) * u.z;
+                d[c + 3] = (d[c + 3] + d2[c + 3]) * u.w;
+              }
             } else {
               tc::tmem_wait_ld();
             }
@@ -1442,23 +1427,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // device-wide, count this contributor in.  The last of an item's contributors merges
     // it, after its range.
     if constexpr (FP8) {
-      int* w_max = reinterpret_cast<int*>(qsc) + 18;  // [2]
       Cursor cq;
       cq.init(u0, S);
       int left = T - (cq.tb - cq.t);
       for (int n = 1; left > 0; ++n) {
         const int qb = n & 1;
         cq.next_item(S);
-        const float unit = split_q<NQ, DH, 2>(
+        split_q<NQ, DH, 2>(
             static_cast<const __nv_bfloat16*>(p.q) + row_of(cq.qc, cq.b, cq.h), col_off,
-            columns(cq.qc, cq.b), warp - 2, q_buf + qb * C::kQParts * C::kQPart, [&](uint32_t mx) {
-              tc::named_bar_sync(7, 64);  // the last call's are read
-              if (lane == 0) w_max[warp - 2] = (int)mx;
-              tc::named_bar_sync(7, 64);
-              return (uint32_t)max(w_max[0], w_max[1]);
-            },
+            columns(cq.qc, cq.b), warp - 2, q_buf + qb * C::kQParts * C::kQPart, qsc + qb * 32,
             [&] { wait_bar(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status); });
-        if (warp == 2 && lane == 0) qsc[qb] = unit;
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&q_full[qb]);

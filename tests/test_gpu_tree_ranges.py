@@ -147,3 +147,38 @@ def test_rows_of_zeros(F):
     c.call(F)
     check_rows(c)
     assert (c.t["out"][0] == 0).all()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("exp", [12, 20, 60])
+def test_queries_of_different_size(F, shape, exp):
+    """One node's queries, and one head's, far above and below the others': each row is as
+    exact as if it were alone."""
+    c = Case("fp8", *shape, seed=15)
+    c.q[:, 4] = (c.q[:, 4].float() * 2.0 ** exp).to(torch.bfloat16)
+    c.q[:, :, 1] = (c.q[:, :, 1].float() * 2.0 ** -exp).to(torch.bfloat16)
+    c.dev(F)
+    from_device(c)
+    c.call(F)
+    seqs = range(0, c.B, max(1, c.B // 4))
+    rows = np.ones((c.B, c.T), bool)
+    rows[:, 4] = False  # its scores are beyond what an exponent is formed from
+    check_rows(c, rows, seqs)
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite(F, what):
+    """It makes its own row NaN and no other."""
+    c = Case("fp8", 2, 600, 8, 2, 128, 9, [500, 33], seed=16)
+    c.q[:, 4, 3, 17] = what
+    c.dev(F)
+    c.q[:, 4, 3, 17] = 0.0  # for the oracle
+    from_device(c)
+    c.call(F)
+    got = O.to_f64(c.t["out"].cpu()).reshape(c.B, c.T, c.Hq, c.dh)
+    assert np.isnan(got[:, 4, 3]).all()
+    got[:, 4, 3] = 0.0
+    assert np.isfinite(got).all()
+    rows = np.ones((c.B, c.T), bool)
+    rows[:, 4] = False
+    check_rows(c, rows)
