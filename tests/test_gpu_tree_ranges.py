@@ -182,3 +182,44 @@ def test_a_query_that_is_not_finite(F, what):
     rows = np.ones((c.B, c.T), bool)
     rows[:, 4] = False
     check_rows(c, rows)
+
+
+@pytest.mark.parametrize("shape", SHAPES + [(2, 600, 1, 1, 128, 3, [500, 3]), (3, 400, 2, 2, 64, 4, [390, 0, 7])])
+def test_single_elements_that_are_nan(F, shape):
+    """An 8-bit v of a node with NaN in single elements: NaN in exactly those of the nodes that
+    see it, whole items and merged ones, and every other element as it should be."""
+    c = Case("fp8", *shape, seed=17)
+    bad = 1
+    where = [3, c.dh - 1]
+    for b in range(c.B):
+        slot = int(c.lens[b]) + bad
+        bits = c.v.view(torch.uint8)
+        bits[b, c.Hkv - 1, slot, where[0]] = 0x7f
+        bits[b, c.Hkv - 1, slot, where[1]] = 0xff
+    c.dev(F)
+    from_device(c)
+    c.call(F)
+    assert F.fdllm_get_status(c.ws) == F.OK
+    torch.cuda.synchronize()
+    got = O.to_f64(c.t["out"].cpu()).reshape(c.B, c.T, c.Hkv, c.Hq // c.Hkv, c.dh)
+    see = np.stack([O.ancestors(p, c.T)[:, bad] for p in c.parent])
+    want = np.zeros(got.shape, bool)
+    for d in where:
+        want[:, :, c.Hkv - 1, :, d] = see[..., None]
+    assert (np.isnan(got) == want).all()
+    assert np.isfinite(got[~want]).all()
+    # the rest: as if the elements were zeros
+    out = c.t["out"]
+    out[torch.isnan(out)] = 0.0
+    c.v_val[np.isnan(c.v_val)] = 0.0
+    c.v64[np.isnan(c.v64)] = 0.0
+    seqs = range(0, c.B, max(1, c.B // 4))
+    # (the oracle's zero where NaN was put to 0; other elements of those rows are compared too)
+    res = O.to_f64(out.cpu()).reshape(c.B, c.T, c.Hq, c.dh)
+    q64 = O.to_f64(c.q)
+    for b in seqs:
+        ref, _, _ = O.tree_attend(q64[b], c.k64[b], c.v64[b], int(c.lens[b]), c.parent[b], c.T)
+        hit = want[b].reshape(c.T, c.Hq, c.dh)
+        res[b][hit] = ref[hit]
+    out.copy_(torch.from_numpy(res.reshape(out.shape)).to(out.dtype))
+    check_rows(c, None, seqs)
