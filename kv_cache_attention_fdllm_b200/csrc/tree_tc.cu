@@ -162,6 +162,7 @@ struct Misc {
 struct Ints {
   uint32_t tmem;
   int abort;
+  int done;           // tiles of the range whose last product is issued
   int merge_u[2];     // first unit of the item in partial slot s that this CTA merges, or -1
   // a closed segment, by O buffer and group: has the group tiles in it, did it meet a node's
   // V that is not finite
@@ -496,6 +497,23 @@ struct IdleClock {
   }
 };
 
+// Waits for something that may take a whole item or range: for as long as *done moves, and
+// kWaitLimitNs from when it stands still.
+__device__ __noinline__ bool wait_while_moving(uint64_t* bar, uint32_t parity, const volatile int* done,
+                                               volatile int* abort, int* status) {
+  IdleClock clk;
+  int seen = *done;
+  while (!tc::mbar_try_wait(bar, parity)) {
+    const int now = *done;
+    if (now != seen) {
+      seen = now;
+      clk.reset();
+    }
+    if (!clk.idle(abort, status)) return false;
+  }
+  return true;
+}
+
 // First unit of CTA c's range, and the CTA whose range holds unit u (the largest c
 // with lo(c) <= u; a double-precision estimate is put right with exact products).
 __device__ __forceinline__ int unit_lo(int total, int G, int c) {
@@ -625,6 +643,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       tc::mbar_init(&fin_full[b], kSmx / 32);
     }
     I->abort = 0;
+    I->done = 0;
     I->bad_run[0] = I->bad_run[1] = 0;
     tc::fence_mbar_init();
   }
@@ -897,6 +916,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           if (leader) {
             tc::mma_commit(&pv_done[ip & 1]);
             tc::mma_commit(&v_empty[vs]);
+            *reinterpret_cast<volatile int*>(&I->done) = ip + 1;
           }
           if (++vs == NV) {
             vs = 0;
@@ -1436,7 +1456,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         split_q<NQ, DH, 2>(
             static_cast<const __nv_bfloat16*>(p.q) + row_of(cq.qc, cq.b, cq.h), col_off,
             columns(cq.qc, cq.b), warp - 2, q_buf + qb * C::kQParts * C::kQPart, qsc + qb * 32,
-            [&] { wait_bar(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, abort_flag, p.status); });
+            [&] {
+              wait_while_moving(&q_empty[qb], ((uint32_t)(n >> 1) & 1u) ^ 1u, &I->done, abort_flag,
+                                p.status);
+            });
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&q_full[qb]);
@@ -1456,13 +1479,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const int tb = slot == 0 ? ca.tb : cz.tb;
           if (slot == 1 && iu == u0 - ca.t) break;
           if (u0 <= iu && u1 >= iu + tb) continue;  // whole: the softmax warps write it
-          bool ready = false;
-          IdleClock clk;
-          while (!(ready = tc::mbar_test(&fin_full[slot], 0u))) {
-            __nanosleep(64);
-            if (!clk.idle(abort_flag, p.status)) break;
-          }
-          if (!ready) break;
+          if (!wait_while_moving(&fin_full[slot], 0u, &I->done, abort_flag, p.status)) break;
           fence_gpu();
           const int c_first = owner_of(iu, U, G), c_last = owner_of(iu + tb - 1, U, G);
           // an item that goes on behind CTA c_first's range is the only one to do so, so
