@@ -7,11 +7,13 @@ non-OK status.  The library launches on the current CUDA device, so the tensors
 and the stream must be on it (a ValueError otherwise).  Every step of the
 computation runs in the CUDA library.  The calls for drafted tokens, where host
 time counts, are checked and made in C++ when they fit (_fast); what does not
-fit comes back to the checks here, which say why.
+fit comes back to the checks here, which say why.  Without _fast.so all of them
+go through the checks here.
 """
 from __future__ import annotations
 
 import ctypes
+import warnings
 
 import torch
 
@@ -20,8 +22,11 @@ from ._native import lib
 try:
     from . import _fast
 except ImportError as e:
-    raise ImportError("_fast.so is missing or was built for another torch: build it with "
-                      "`python kv_cache_attention_fdllm_b200/build.py`") from e
+    # every call works without it, those for drafted tokens with 6 us more of host time
+    _fast = None
+    warnings.warn("_fast.so is missing or was built for another torch, calls for drafted tokens take "
+                  f"the slower way: build it with `python kv_cache_attention_fdllm_b200/build.py` ({e})",
+                  RuntimeWarning)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_BAD_INDEX, ERR_TIMEOUT, ERR_WORKSPACE = range(7)
 FLAG_COMMIT, FLAG_ACCEPT, FLAG_PASS = 1, 2, 4
@@ -396,7 +401,7 @@ def fdllm_cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scal
 
     k_rows, v_rows [B, R, H, dh]; pos int32 [B, R], -1 skips a row; the caches
     float8_e4m3fn [B, H, N, dh] with float32 scales [B, H, N], updated in place."""
-    if stream is None:
+    if stream is None and _fast is not None:
         st = _fast.cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
         if st >= 0:
             _check(st, "fdllm_cache_write_fp8")
@@ -412,7 +417,7 @@ def fdllm_cache_write_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scal
 def fdllm_cache_read_fp8(pos, k_cache, v_cache, k_scale, v_scale, k_rows, v_rows, workspace,
                          stream=None):
     """Rows of an 8-bit cache read back into k_rows, v_rows [B, R, H, dh] (see include/fdllm.h)."""
-    if stream is None:
+    if stream is None and _fast is not None:
         st = _fast.cache_read_fp8(k_rows, v_rows, pos, k_cache, v_cache, k_scale, v_scale, workspace)
         if st >= 0:
             _check(st, "fdllm_cache_read_fp8")
@@ -452,7 +457,7 @@ def fdllm_tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, work
 
     q [B, T, Hq, dh]; caches [B, Hkv, N, dh]; cache_len int32 [B]; parent int32
     [B, T] or None (a chain); n_nodes int32 [B] or None (T); out [B, T, Hq*dh]."""
-    if stream is None:
+    if stream is None and _fast is not None:
         st = _fast.tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, workspace)
         if st >= 0:
             _check(st, "fdllm_tree_attend")
@@ -469,7 +474,7 @@ def fdllm_tree_attend(q, k_cache, v_cache, cache_len, parent, n_nodes, out, work
 def fdllm_tree_attend_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_len, parent, n_nodes, out,
                           workspace, stream=None):
     """fdllm_tree_attend over an 8-bit cache (float8_e4m3fn, float32 scales [B, Hkv, N])."""
-    if stream is None:
+    if stream is None and _fast is not None:
         st = _fast.tree_attend_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_len, parent,
                     n_nodes, out, workspace)
         if st >= 0:
@@ -494,7 +499,7 @@ def fdllm_chain_verify(target, draft, tok, n_draft, u, r, n_accept, next_tok, wo
     target float32 [B, T+1, V], draft float32 [B, T, V], tok int32 [B, T], n_draft
     int32 [B] or None (T), u float32 [B, T], r float32 [B]; n_accept, next_tok
     int32 [B] (out)."""
-    if stream is None:
+    if stream is None and _fast is not None:
         st = _fast.chain_verify(target, draft, tok, n_draft, u, r, n_accept, next_tok, workspace)
         if st >= 0:
             _check(st, "fdllm_chain_verify")
@@ -529,7 +534,7 @@ def fdllm_tree_verify(target, tok, parent, n_nodes, u, r, path, n_accept, next_t
     target float32 [B, T, V], tok and parent int32 [B, T], n_nodes int32 [B] or
     None (T), u float32 [B, T], r float32 [B]; path int32 [B, T], n_accept and
     next_tok int32 [B] (out)."""
-    if stream is None:
+    if stream is None and _fast is not None:
         st = _fast.tree_verify(target, tok, parent, n_nodes, u, r, path, n_accept, next_tok,
                     workspace)
         if st >= 0:
