@@ -21,6 +21,8 @@ from ._native import lib
 
 try:
     from . import _fast
+    if _fast.torch_version != torch.__version__.split("+")[0]:
+        raise ImportError(f"it was built for torch {_fast.torch_version}")
 except ImportError as e:
     # every call works without it, those for drafted tokens with 6 us more of host time
     _fast = None

@@ -24,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfdllm.so")
 FAST = os.path.join(PKG, "_fast.so")
+FAST_FOR = os.path.join(BUILD, "fast_for.txt")  # what FAST was built for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -47,9 +48,28 @@ def _headers_mtime():
     return max((os.path.getmtime(h) for h in hs), default=0.0)
 
 
-def _fast_command(cc) -> list:
+def _torch() -> str:
     # found, not imported: importing torch takes longer than the compilation it is for
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _fast_made_for() -> str:
+    """What a _fast.so belongs to: the torch it is compiled against and the interpreter."""
+    with open(os.path.join(_torch(), "version.py")) as f:
+        return f"{_torch()}\n{f.read()}\n{sys.version}\n"
+
+
+def _fast_stale() -> bool:
+    src = os.path.join(CSRC, "fast_call.cpp")
+    if not os.path.exists(FAST) or not os.path.exists(FAST_FOR) or \
+            os.path.getmtime(FAST) < max(os.path.getmtime(src), _headers_mtime()):
+        return True
+    with open(FAST_FOR) as f:
+        return f.read() != _fast_made_for()
+
+
+def _fast_command(cc) -> list:
+    torch = _torch()
     inc = os.path.join(torch, "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(cc)), "include")
     libs = os.path.join(torch, "lib")
@@ -93,9 +113,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         cmd = [cc] + ARCH + ["-shared", "-o", LIB] + objs + ["-lcudart_static", "-ldl", "-lrt",
                                                                "-lpthread"]
         run(cmd)
-    src = os.path.join(CSRC, "fast_call.cpp")
-    if force or not os.path.exists(FAST) or os.path.getmtime(FAST) < max(os.path.getmtime(src), hdr):
+    if force or _fast_stale():
         run(_fast_command(cc))
+        with open(FAST_FOR, "w") as f:
+            f.write(_fast_made_for())
     return LIB
 
 

@@ -4,6 +4,7 @@
 // does not fit goes back to them (-1), and they say why.  No check is left out: a call is
 // made here only where each of theirs would pass.
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -214,4 +215,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fast() { return PyModule_Create(&module); }
+// torch_version: of the headers that this was compiled against, whose layouts it relies on
+PyMODINIT_FUNC PyInit__fast() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

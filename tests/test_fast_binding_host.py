@@ -52,3 +52,35 @@ print(A._fast.__file__)
 """)
     assert rc == 0, err
     assert out.strip().endswith("_fast.so") and "RuntimeWarning" not in err
+
+
+def test_another_torch_rebuilds_it(tmp_path, monkeypatch):
+    """What was built against another torch is built again; what was not, is not."""
+    import __graft_entry__
+    B = __graft_entry__._build_module()
+    assert not B._fast_stale()
+    made = open(B.FAST_FOR).read()
+    for other in (made.replace(B._torch(), "/elsewhere/torch"), made.replace("__version__ = '", "__version__ = '1"), ""):
+        assert other != made
+        stamp = tmp_path / "fast_for.txt"
+        stamp.write_text(other)
+        monkeypatch.setattr(B, "FAST_FOR", str(stamp))
+        assert B._fast_stale()
+    monkeypatch.setattr(B, "FAST_FOR", str(tmp_path / "none.txt"))
+    assert B._fast_stale()
+
+
+def test_one_of_another_torch_is_not_used():
+    """It may load and still read tensors wrongly."""
+    rc, out, err = python("""
+import sys
+import torch
+import types
+m = types.ModuleType("kv_cache_attention_fdllm_b200._fast")
+m.torch_version = "1.0.0"
+sys.modules[m.__name__] = m
+import kv_cache_attention_fdllm_b200.api as A
+print(A._fast)
+""")
+    assert rc == 0, err
+    assert out.strip() == "None" and "torch 1.0.0" in err
