@@ -77,6 +77,7 @@ int row_dtype(const at::Tensor* t) {
   return t->scalar_type() == ScalarType::Float ? FDLLM_F32 : -1;
 }
 
+// The interpreter's lock is given up around `call`, which must not throw.
 template <typename F>
 PyObject* run(const Call& c, F call) {
   if (!c.ok) return PyLong_FromLong(-1);
@@ -137,6 +138,7 @@ PyObject* tree_attend(PyObject* const* a) {
   const int B = c.dim(q, 0), T = c.dim(q, 1), Hq = c.dim(q, 2), dh = c.dim(q, 3);
   const int Hkv = c.dim(cache, 1), N = c.dim(cache, 2), type = row_dtype(q);
   c.ok = c.ok && type >= 0;
+  const void* qp = c.ok ? q->data_ptr() : nullptr;
   const ScalarType kind = FP8 ? ScalarType::Float8_e4m3fn : q->scalar_type();
   void* kc = c.take(a[1], kind, {B, Hkv, N, dh});
   void* vc = c.take(a[2], kind, {B, Hkv, N, dh});
@@ -151,10 +153,10 @@ PyObject* tree_attend(PyObject* const* a) {
   void* ws = c.workspace(a[4], &bytes);
   return run(c, [&](void* stream) {
     if (FP8)
-      return fdllm_tree_attend_fp8(B, N, Hq, Hkv, dh, T, type, q->data_ptr(), kc, vc, ks, vs, len, parent,
-                                   nodes, out, ws, bytes, stream);
-    return fdllm_tree_attend(B, N, Hq, Hkv, dh, T, type, q->data_ptr(), kc, vc, len, parent, nodes, out,
-                             ws, bytes, stream);
+      return fdllm_tree_attend_fp8(B, N, Hq, Hkv, dh, T, type, qp, kc, vc, ks, vs, len, parent, nodes, out,
+                                   ws, bytes, stream);
+    return fdllm_tree_attend(B, N, Hq, Hkv, dh, T, type, qp, kc, vc, len, parent, nodes, out, ws, bytes,
+                             stream);
   });
 }
 
