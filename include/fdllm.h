@@ -329,8 +329,11 @@ size_t fdllm_tree_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int dh, 
  * No slot past the sequence's nodes is used, whatever it holds; a sibling's NaN
  * or infinity reaches no node that does not see it.  T = 1 is single-token
  * decoding; all nodes of a prompt's chunk may be one chain of T.
- * Hq a multiple of Hkv, at most 64 query heads to a kv head; T at most
- * FDLLM_MAX_TREE_NODES; B at most FDLLM_MAX_TREE_SEQS.  A cache_len or n_nodes
+ * Scores, maxima and sums are fp32.  Over 16- and 8-bit caches the weights are
+ * rounded to 8 and 9 bits before they meet V, except where a kv head has one row (one
+ * node, one query head) or, in calls of few sequences, up to 4: fp32 there.
+ * Hq a multiple of Hkv, at most 4096, and at most 64 query heads to a kv head; T at
+ * most FDLLM_MAX_TREE_NODES; B at most FDLLM_MAX_TREE_SEQS; B * N at most 2^31.  A cache_len or n_nodes
  * out of range (cache_len + n_nodes > N included) sets FDLLM_ERR_BAD_INDEX and
  * that sequence's rows are left as they were; a parent out of range sets it too
  * and counts as -1.  Deterministic. */
@@ -375,8 +378,8 @@ size_t fdllm_draft_verify_workspace_bytes(int B, int T, int V);
  *                                 the row of the first draft not accepted, or the
  *                                 target's row behind the last draft.  A w that is 0
  *                                 everywhere: that row of target itself; 0 too: -1.
- * Products, differences and sums in 64 bits; a NaN counts as 0, and so does a
- * negative weight.  A token outside [0, V) sets FDLLM_ERR_BAD_INDEX and is not
+ * Products, differences and sums in 64 bits; a weight that is negative or NaN counts
+ * as 0, and a comparison with a NaN accepts nothing.  A token outside [0, V) sets FDLLM_ERR_BAD_INDEX and is not
  * accepted; an n_draft out of range sets it too and is brought into [0, T].
  * Deterministic. */
 fdllm_status fdllm_chain_verify(int B, int T, int V, const float* target, const float* draft,

@@ -256,9 +256,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheFp8Args a, in
   }
 }
 
-// Rows of a CTA's block: enough (row, head) pairs for two rounds of its groups,
-// and 16 where a sequence's rows are so many that the scan for replaced rows
-// would otherwise be read too often.
+// Rows of a CTA's block: two (row, head) pairs to a group (one round of the write, which
+// has two in flight; two of the read), and 16 rows where a sequence has so many that the
+// scan for replaced rows would otherwise be read too often.
 int rows_per_block(const CacheFp8Args& a) {
   if (a.R > 1024) return kMaxBlockRows;
   const int groups = kThreads / (a.dh / 8);

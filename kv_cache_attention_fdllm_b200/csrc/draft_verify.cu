@@ -20,8 +20,8 @@
 // launch; its warps then sum sub-blocks of 512 weights, 16-byte loads all in
 // flight before the first is used; the last CTA of the sequence to finish finds
 // the sub-block that holds r sum(w) from the sums, and in it the token.  Measured at a
-// vocabulary of 126464: 8 chains of 5 drafts 8.2 us, 64 of 4 16.5 us (64.8 MB), 8 trees of
-// 40 nodes 10.2 us; of the 8.2 us the walk takes 1.5, the sums 2.6, the count 1, the draw
+// vocabulary of 126464: 8 chains of 5 drafts 8.2 us, 64 of 4 16.4-18.0 us (64.8 MB; the more
+// the less of them L2 holds), 8 trees of 40 nodes 10.3 us; of the 8.2 us the walk takes 1.5, the sums 2.6, the count 1, the draw
 // 2.8, each a dependent round trip or two.
 #include <limits.h>
 
@@ -361,8 +361,8 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(DraftVerifyAr
 }
 
 // CTAs of a sequence: four a SM over all of them, which is what is resident (one CTA more
-// a sequence and the last start when the first end: 20.6 us in place of 17.8 for 64 chains
-// of 4 drafts over 126464 tokens), no more than one round of sub-blocks each.
+// a sequence and the last start when the first end: 20.6 us for 17.8, measured together, for
+// 64 chains of 4 drafts over 126464 tokens), no more than one round of sub-blocks each.
 int ctas_per_seq(int B, int V) {
   const int n_sub = (V + kSub - 1) / kSub;
   const int most = (n_sub + kWarps - 1) / kWarps;

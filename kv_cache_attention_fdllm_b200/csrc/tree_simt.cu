@@ -16,8 +16,8 @@
 //
 // Bound by latency over a short cache: launch, length, one round trip for K and V, the join
 // (one token, 32 heads, 1024 slots: 8.2 us, of which the bytes are 2.5); one row over a large
-// one runs at the rate of its loads (64 sequences of 4096, 32 heads, 4.3 GB in 16 bits: 597
-// us, 7.2 TB/s; in 8 bits 376 us).  More rows are bound by instructions, some 450 a step of
+// one runs at the rate of its loads (64 sequences of 4096, 32 heads, 4.3 GB in 16 bits: 598
+// us, 7.2 TB/s; in 8 bits 373 us).  More rows are bound by instructions, some 450 a step of
 // 8 slots at 4 rows, and beyond them the tensor cores' kernel takes over; fp32 has none, and
 // nothing large runs there.
 #include <atomic>
@@ -564,11 +564,13 @@ cudaError_t launch_c(const TreeAttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // fp32; one row to a kv head, whatever the size (one sequence of 1024, 32 kv heads: 8.2 us,
-// on the tensor cores 20.5; 64 of 4096: 597 for 647 in 16 bits, 376 for 589 in 8); up to 4
+// on the tensor cores 21.9; 64 of 4096: 598 for 650 in 16 bits, 373 for 573 in 8); up to 4
 // rows where the sequences' kv heads are few, so that latency counts (4 rows, 8 kv heads, 16
-// and 8 bits: 1 x 1024 10 for 16 and 10 for 22, 8 x 4096 35 for 36 and 38 for 43, 8 x 16384
-// 98 for 96 and 109 for 89).  With more of them the instructions of 4 rows cost more than the
-// tensor cores' kernel takes (64 x 4096: 200 for 174, 203 for 164).
+// and 8 bits: 1 x 1024 12.3 for 16.4 and 12.3 for 20.5, 8 x 4096 38.9 for 36.5 and 40.5 for
+// 41.0).  The lengths are on the device, so that the rule cannot know them: 8 of 16384 lose
+// by it (100.7 for 96.2, 109.9 for 86.1).  With more heads the instructions of 4 rows cost
+// more than the tensor cores' kernel takes (64 x 4096: 186 for 176, 208 for 160; 2 rows of 16
+// bits 195 for 175, of 8 bits 155 for 159).
 bool tree_simt_takes(const TreeAttnArgs& a) {
   const int rows = a.T * (a.Hq / a.Hkv);
   return a.dtype == FDLLM_F32 || rows == 1 || (rows <= 4 && a.B * a.Hkv <= 64);

@@ -45,9 +45,10 @@
 //
 // Measured (head size 128, times of calls back to back).  16 bits: 64 sequences of 4096, 32
 // heads of 32 nodes, 4.3 GB: 650-713 us, the memory's rate; 8 of up to 2000, 32 heads of 40
-// nodes, 239 MB: 60 us, of which 37 are bytes and the rest a CTA's first tile, its two segment
+// nodes, 239 MB: 61 us, of which 37 are bytes and the rest a CTA's first tile, its two segment
 // ends and merges.  8 bits, 8 kv heads of 32 rows: 64 sequences of 1000-4080, 343 MB: 129 us;
-// 8 of 16384, 278 MB: 89 us: 2000-2300 cycles a tile, some 10000 more a segment.
+// 8 of 16384, 278 MB: 88 us: 2000-2300 cycles a tile, some 10000 more a segment.  (The 8-bit
+// instances spill some 50 bytes a thread: 640 threads leave 96 registers each.)
 //
 // O^T is double-buffered in TMEM (once for each group): an item's result is written
 // some tiles into the next item, off the softmax path.
